@@ -98,6 +98,31 @@ typedef struct {
     const float* W_down_s;
 } moe_weights_fp8_t;
 
+/* 4-bit weights with group scales (see moe_quantize_w4): the matrix w[n][k] of every expert as codes
+ * q [E][n][k / 2], scales s [E][G][n] bf16 and zero points z [E][G][n] (NULL: 8 everywhere), where one scale
+ * and zero point serve `group` consecutive columns of a row and G = ceil(k / group):
+ *   w[e][n][j] = (code(e, n, j) - z[e][j / group][n]) * s[e][j / group][n]
+ * Eight columns of a row are one little-endian 32-bit word: nibble i (0..3) holds column 2 i, nibble 4 + i
+ * column 2 i + 1.  Where (code - z) * s needs more than bf16's 8 significant bits it is rounded to bf16 (to
+ * nearest even) before the products; with moe_quantize_w4's scales it never does. */
+typedef struct {
+    const uint8_t* q;
+    const void* s;
+    const uint8_t* z;
+} moe_w4_t;
+
+/* 4-bit expert weights: W_gate and W_up (n = d_ff, k = d), W_down (n = d, k = d_ff), one group size (32, 64
+ * or 128); W_gate and W_up both have zero points or neither has.  gamma, W_r and b as in moe_weights_t. */
+typedef struct {
+    const float* gamma;
+    const float* W_r;
+    const float* b;
+    moe_w4_t W_gate;
+    moe_w4_t W_up;
+    moe_w4_t W_down;
+    int32_t group;
+} moe_weights_w4_t;
+
 /*
  * Step 1 — RMSNorm [P1 §Norm&Residual, RMSNorm equation]:
  *   v[t][j] = gamma[j] * x[t][j] / sqrt((1/d) * sum_k x[t][k]^2 + eps)
@@ -346,6 +371,67 @@ moe_status_t moe_grouped_swiglu_fp8(const uint8_t* xq, const float* xs, const mo
 moe_status_t moe_forward_fp8(const moe_shape_t* shape, const moe_weights_fp8_t* w, const void* x, void* out,
                              int32_t* topk_idx, float* topk_w, float* logits, void* ws, size_t* ws_bytes,
                              int32_t* dev_status, moe_stream_t stream);
+
+/*
+ * 4-bit quantisation with group scales (the pages name no 4-bit experts; a convenience of this library beside
+ * the block-FP8 experts).  x [E][n][k] (MOE_F32 or MOE_BF16) -> q, s, z as moe_w4_t lays them out:
+ *   z == NULL: s = up5(max|x| / 7), code = clamp(rint(x / s), -8, 7) + 8
+ *   else:      lo = min(0, min x), hi = max(0, max x), s = up4((hi - lo) / 15),
+ *              z = clamp(rint(-lo / s), 0, 15), code = clamp(rint(x / s) + z, 0, 15)
+ * over the columns of a group; up5 / up4 is the least number of 5 / 4 significant bits that is not smaller
+ * (at least 2^-100), so (code - z) * s is a bf16 exactly.  Quotients are rounded exactly, to nearest even.  A
+ * group of zeros gets s = 1.  A group holding a value that is not finite, or of magnitude 2^120 or more, gets
+ * s = NaN.  group 32, 64 or 128 (the last group of a row may be short); k % 32 == 0; E <= 65535; x and q
+ * 16-byte aligned.
+ */
+moe_status_t moe_quantize_w4(const void* x, moe_dtype_t dt, int32_t E, int64_t n, int32_t k, int32_t group, uint8_t* q,
+                             void* s, uint8_t* z, moe_stream_t stream);
+
+/* The weights that codes, scales and zero points stand for: out [E][n][k] (out_dt) = (code - z) * s, rounded to
+ * out_dt.  With MOE_BF16 these are the weights of the products below. */
+moe_status_t moe_dequantize_w4(const moe_w4_t* w, int32_t E, int64_t n, int32_t k, int32_t group, void* out,
+                               moe_dtype_t out_dt, moe_stream_t stream);
+
+/*
+ * Step 4 with 4-bit experts, the two halves and both [as moe_expert_gate_up, moe_expert_down and
+ * moe_grouped_swiglu]: xp [S][d], h [S][d_ff], y [S][d] bf16, any rows per expert, fp32 sums; h and y are
+ * rounded once.  Segments that do not fit the S rows are clamped and flagged as there; rows outside every
+ * segment are not written.  Requires d % 32 == 0, d_ff % 32 == 0, d and d_ff <= MOE_W4_MAX_DIM, E <= 256; q, s
+ * and z 16-byte aligned.
+ */
+#define MOE_W4_MAX_DIM 16384
+moe_status_t moe_expert_gate_up_w4(const void* xp, const moe_w4_t* W_gate, const moe_w4_t* W_up, int32_t group,
+                                   const int32_t* counts, const int32_t* offsets, int32_t S, int32_t E, int32_t d,
+                                   int32_t d_ff, void* h, int32_t* dev_status, moe_stream_t stream);
+moe_status_t moe_expert_down_w4(const void* h, const moe_w4_t* W_down, int32_t group, const int32_t* counts,
+                                const int32_t* offsets, int32_t S, int32_t E, int32_t d, int32_t d_ff, void* y,
+                                int32_t* dev_status, moe_stream_t stream);
+moe_status_t moe_grouped_swiglu_w4(const void* xp, const moe_weights_w4_t* w, const int32_t* counts,
+                                   const int32_t* offsets, int32_t S, int32_t E, int32_t d, int32_t d_ff, void* h,
+                                   void* y, int32_t* dev_status, moe_stream_t stream);
+
+/*
+ * Steps 3-5 with 4-bit experts for a few tokens, straight from the router's picks, without a permutation:
+ *   out[t] = residual[t] + sum_{i<k} topk_w[t][i] * MLP_{topk_idx[t][i]}(v[t]),
+ *   MLP_e(v) = (SiLU(v W_gate[e]^T) * (v W_up[e]^T)) W_down[e]^T
+ * v [T][d] bf16, topk_idx / topk_w [T][k], residual [T][d] (r_dt), out [T][d] (out_dt; may be residual).  The
+ * intermediate is carried with 16 significant bits and everything after it in fp32, so an fp32 output is that
+ * precise.  A pick with a bad expert id is left out and sets MOE_DEV_BAD_EXPERT_ID.  A token may name an
+ * expert twice.  T * k <= MOE_W4_MAX_PICKS, k <= 8, sizes as above; the workspace holds the intermediates.
+ */
+#define MOE_W4_MAX_PICKS 256
+moe_status_t moe_picks_swiglu_w4(const void* v, const moe_weights_w4_t* w, const int32_t* topk_idx, const float* topk_w,
+                                 const void* residual, moe_dtype_t r_dt, int32_t T, int32_t k, int32_t E, int32_t d,
+                                 int32_t d_ff, void* out, moe_dtype_t out_dt, void* ws, size_t* ws_bytes,
+                                 int32_t* dev_status, moe_stream_t stream);
+
+/*
+ * The whole layer with 4-bit experts: as moe_forward with the expert MLP in 4-bit weights (shape->w_dtype is
+ * ignored).  The normalised rows are rounded to bf16 for the experts; few tokens run moe_picks_swiglu_w4.
+ */
+moe_status_t moe_forward_w4(const moe_shape_t* shape, const moe_weights_w4_t* w, const void* x, void* out,
+                            int32_t* topk_idx, float* topk_w, float* logits, void* ws, size_t* ws_bytes,
+                            int32_t* dev_status, moe_stream_t stream);
 
 /*
  * Expert parallelism over peer memory (steps 3 and 5 fused with their

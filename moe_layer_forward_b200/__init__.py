@@ -10,7 +10,9 @@ package fails loudly if ``libmoe.so`` has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -45,7 +47,26 @@ class MoeWeightsFP8(ctypes.Structure):
                 ("W_up_s", _vp), ("W_down_q", _vp), ("W_down_s", _vp)]
 
 
+class MoeW4(ctypes.Structure):
+    _fields_ = [("q", _vp), ("s", _vp), ("z", _vp)]
+
+
+class MoeWeightsW4(ctypes.Structure):
+    _fields_ = [("gamma", _vp), ("W_r", _vp), ("b", _vp), ("W_gate", MoeW4), ("W_up", MoeW4), ("W_down", MoeW4),
+                ("group", _i32)]
+
+
+_w4p, _ww4p = ctypes.POINTER(MoeW4), ctypes.POINTER(MoeWeightsW4)
+
 _sig = {
+    "moe_quantize_w4": [_vp, _i32, _i32, _i64, _i32, _i32, _vp, _vp, _vp, _vp],
+    "moe_dequantize_w4": [_w4p, _i32, _i64, _i32, _i32, _vp, _i32, _vp],
+    "moe_expert_gate_up_w4": [_vp, _w4p, _w4p, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp],
+    "moe_expert_down_w4": [_vp, _w4p, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp],
+    "moe_grouped_swiglu_w4": [_vp, _ww4p, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp],
+    "moe_picks_swiglu_w4": [_vp, _ww4p, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _szp, _vp,
+                            _vp],
+    "moe_forward_w4": [ctypes.POINTER(MoeShape), _ww4p, _vp, _vp, _vp, _vp, _vp, _vp, _szp, _vp, _vp],
     "moe_rmsnorm": [_vp, _i32, _vp, _i32, _i32, _f32, _vp, _i32, _vp],
     "moe_router_topk": [_vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _szp, _vp],
     "moe_route": [_vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp, _szp, _vp],
@@ -389,3 +410,239 @@ def moe_forward_fp8(x, gamma, W_r, b, Wg, Wu, Wd, out, top_k: int = 8, eps: floa
                                                    _p(topk_w), _p(logits), _p(ws), ctypes.byref(n), _p(dev_status),
                                                    _stream(x.device)))
 
+
+
+# --------------------------------------------------------------------------- 4-bit experts
+class W4Weights(NamedTuple):
+    """A 4-bit expert matrix [E][n][k]: codes q uint8 [E][n][k / 2], scales s bf16 and zero points z uint8 (or None: 8
+    everywhere) [E][ceil(k / group)][n]; see ``moe_w4_t`` in include/moe.h for the layout and ``pack_w4``."""
+
+    q: torch.Tensor
+    s: torch.Tensor
+    z: Optional[torch.Tensor]
+    group: int
+
+
+def pack_w4(codes: torch.Tensor) -> torch.Tensor:
+    """Codes 0..15 [..., k] (uint8, k % 8 == 0) as the packed bytes [..., k / 2] of W4Weights.q."""
+    c = codes.reshape(*codes.shape[:-1], -1, 8)
+    low, high = c[..., [0, 4, 1, 5]], c[..., [2, 6, 3, 7]]
+    return (low | (high << 4)).to(torch.uint8).reshape(*codes.shape[:-1], -1)
+
+
+def unpack_w4(q: torch.Tensor) -> torch.Tensor:
+    """Codes 0..15 [..., k] of packed bytes [..., k / 2]."""
+    b = q.reshape(*q.shape[:-1], -1, 4)
+    c = torch.cat([b & 15, b >> 4], dim=-1)[..., [0, 2, 4, 6, 1, 3, 5, 7]]
+    return c.reshape(*q.shape[:-1], -1)
+
+
+def _current_device(fn):
+    """Run a call on the device of its first argument, whichever device is current."""
+
+    @functools.wraps(fn)
+    def call(first, *args, **kwargs):
+        dev = (first.q if isinstance(first, W4Weights) else first).device
+        if dev.type != "cuda" or dev.index == torch.cuda.current_device():
+            return fn(first, *args, **kwargs)
+        with torch.cuda.device(dev):
+            return fn(first, *args, **kwargs)
+
+    return call
+
+
+def _expect(name: str, t: torch.Tensor, shape, dtype, device) -> None:
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _w4(name: str, w: W4Weights, E: int, n: int, k: int, device) -> MoeW4:
+    G = -(-k // w.group)
+    _expect(name + ".q", w.q, (E, n, k // 2), torch.uint8, device)
+    _expect(name + ".s", w.s, (E, G, n), torch.bfloat16, device)
+    if w.z is not None:
+        _expect(name + ".z", w.z, (E, G, n), torch.uint8, device)
+    return MoeW4(_p(w.q), _p(w.s), _p(w.z))
+
+
+def _w4_weights(gamma, W_r, b, Wg, Wu, Wd, E, d, d_ff, device) -> MoeWeightsW4:
+    if not Wg.group == Wu.group == Wd.group:
+        raise ValueError("W_gate, W_up and W_down must have one group size")
+    return MoeWeightsW4(_p(gamma), _p(W_r), _p(b), _w4("W_gate", Wg, E, d_ff, d, device),
+                        _w4("W_up", Wu, E, d_ff, d, device), _w4("W_down", Wd, E, d, d_ff, device), Wg.group)
+
+
+def _segments(counts, offsets, E, status, device) -> None:
+    _expect("counts", counts, (E,), torch.int32, device)
+    _expect("offsets", offsets, (E + 1,), torch.int32, device)
+    _status(status, device)
+
+
+def _status(status, device) -> None:
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1 or status.device != device):
+        raise ValueError("dev_status must hold an int32 on the tensors' device")
+
+
+@_current_device
+def moe_quantize_w4(W, w4: W4Weights) -> None:
+    """Codes, scales and (unless w4.z is None) zero points of the matrices W [E][n][k] (f32 or bf16), into w4's tensors."""
+    E, n, k = W.shape
+    o = _w4("w4", w4, E, n, k, W.device)
+    _check("moe_quantize_w4", _lib.moe_quantize_w4(_p(W), _dt(W), E, n, k, w4.group, o.q, o.s, o.z, _stream(W.device)))
+
+
+def quantize_w4_weights(W, group: int = 128, zero: bool = False) -> W4Weights:
+    """4-bit form of an expert weight tensor [E][n][k], on its device (zero: with zero points)."""
+    E, n, k = W.shape
+    if group not in (32, 64, 128) or k % 32 != 0:
+        raise ValueError("group must be 32, 64 or 128 and k a multiple of 32")
+    G = -(-k // group)
+    w4 = W4Weights(torch.empty((E, n, k // 2), dtype=torch.uint8, device=W.device),
+                   torch.empty((E, G, n), dtype=torch.bfloat16, device=W.device),
+                   torch.empty((E, G, n), dtype=torch.uint8, device=W.device) if zero else None, group)
+    moe_quantize_w4(W, w4)
+    return w4
+
+
+@_current_device
+def moe_dequantize_w4(w4: W4Weights, out) -> None:
+    """The weights [E][n][k] that w4 stands for, into out (f32 or bf16)."""
+    E, n, k = out.shape
+    w = _w4("w4", w4, E, n, k, out.device)
+    _check("moe_dequantize_w4", _lib.moe_dequantize_w4(ctypes.byref(w), E, n, k, w4.group, _p(out), _dt(out),
+                                                       _stream(out.device)))
+
+
+@_current_device
+def moe_expert_gate_up_w4(xp, Wg: W4Weights, Wu: W4Weights, counts, offsets, h, dev_status=None) -> None:
+    """h = SiLU(xp W_gate^T) * (xp W_up^T) per expert segment, 4-bit weights."""
+    S, d = xp.shape
+    E, d_ff, _ = Wg.q.shape
+    dev = xp.device
+    _expect("xp", xp, (S, d), torch.bfloat16, dev)
+    _expect("h", h, (S, d_ff), torch.bfloat16, dev)
+    _segments(counts, offsets, E, dev_status, dev)
+    if Wg.group != Wu.group:
+        raise ValueError("W_gate and W_up must have one group size")
+    g, u = _w4("W_gate", Wg, E, d_ff, d, dev), _w4("W_up", Wu, E, d_ff, d, dev)
+    _check("moe_expert_gate_up_w4",
+           _lib.moe_expert_gate_up_w4(_p(xp), ctypes.byref(g), ctypes.byref(u), Wg.group, _p(counts), _p(offsets), S, E,
+                                      d, d_ff, _p(h), _p(dev_status), _stream(dev)))
+
+
+@_current_device
+def moe_expert_down_w4(h, Wd: W4Weights, counts, offsets, y, dev_status=None) -> None:
+    """y = h W_down^T per expert segment, 4-bit weights."""
+    S, d_ff = h.shape
+    E, d, _ = Wd.q.shape
+    dev = h.device
+    _expect("h", h, (S, d_ff), torch.bfloat16, dev)
+    _expect("y", y, (S, d), torch.bfloat16, dev)
+    _segments(counts, offsets, E, dev_status, dev)
+    w = _w4("W_down", Wd, E, d, d_ff, dev)
+    _check("moe_expert_down_w4",
+           _lib.moe_expert_down_w4(_p(h), ctypes.byref(w), Wd.group, _p(counts), _p(offsets), S, E, d, d_ff, _p(y),
+                                   _p(dev_status), _stream(dev)))
+
+
+@_current_device
+def moe_grouped_swiglu_w4(xp, Wg: W4Weights, Wu: W4Weights, Wd: W4Weights, counts, offsets, h, y,
+                          dev_status=None) -> None:
+    """The expert MLP over expert-contiguous rows with 4-bit weights: moe_expert_gate_up_w4, then moe_expert_down_w4."""
+    S, d = xp.shape
+    E, d_ff, _ = Wg.q.shape
+    dev = xp.device
+    _expect("xp", xp, (S, d), torch.bfloat16, dev)
+    _expect("h", h, (S, d_ff), torch.bfloat16, dev)
+    _expect("y", y, (S, d), torch.bfloat16, dev)
+    _segments(counts, offsets, E, dev_status, dev)
+    w = _w4_weights(None, None, None, Wg, Wu, Wd, E, d, d_ff, dev)
+    _check("moe_grouped_swiglu_w4",
+           _lib.moe_grouped_swiglu_w4(_p(xp), ctypes.byref(w), _p(counts), _p(offsets), S, E, d, d_ff, _p(h), _p(y),
+                                      _p(dev_status), _stream(dev)))
+
+
+def picks_w4_workspace_bytes(v, Wg: W4Weights, Wd: W4Weights, topk_idx) -> int:
+    """Bytes of workspace ``moe_picks_swiglu_w4`` needs for these tensors (queues nothing)."""
+    T, d = v.shape
+    E, d_ff, _ = Wg.q.shape
+    w = MoeWeightsW4()
+    w.group = Wd.group
+    n = ctypes.c_size_t(0)
+    _check("moe_picks_swiglu_w4",
+           _lib.moe_picks_swiglu_w4(None, ctypes.byref(w), None, None, None, MOE_F32, T, topk_idx.shape[1], E, d, d_ff,
+                                    None, MOE_F32, None, ctypes.byref(n), None, None))
+    return int(n.value)
+
+
+@_current_device
+def moe_picks_swiglu_w4(v, Wg: W4Weights, Wu: W4Weights, Wd: W4Weights, topk_idx, topk_w, residual, out, ws=None,
+                        dev_status=None) -> None:
+    """out = residual + sum_i topk_w[:, i] MLP_{topk_idx[:, i]}(v) with 4-bit experts, for few tokens (T k <= 256)."""
+    T, d = v.shape
+    E, d_ff, _ = Wg.q.shape
+    k = topk_idx.shape[1]
+    dev = v.device
+    _expect("v", v, (T, d), torch.bfloat16, dev)
+    _expect("topk_idx", topk_idx, (T, k), torch.int32, dev)
+    _expect("topk_w", topk_w, (T, k), torch.float32, dev)
+    _expect("residual", residual, (T, d), residual.dtype, dev)
+    _expect("out", out, (T, d), out.dtype, dev)
+    _status(dev_status, dev)
+    w = _w4_weights(None, None, None, Wg, Wu, Wd, E, d, d_ff, dev)
+    if ws is None:
+        ws = torch.empty(max(picks_w4_workspace_bytes(v, Wg, Wd, topk_idx), 1), dtype=torch.uint8, device=dev)
+    n = ctypes.c_size_t(ws.numel() * ws.element_size())
+    _check("moe_picks_swiglu_w4",
+           _lib.moe_picks_swiglu_w4(_p(v), ctypes.byref(w), _p(topk_idx), _p(topk_w), _p(residual), _dt(residual), T, k,
+                                    E, d, d_ff, _p(out), _dt(out), _p(ws), ctypes.byref(n), _p(dev_status),
+                                    _stream(dev)))
+
+
+def _shape_w4(x, Wg: W4Weights, out, top_k, eps) -> MoeShape:
+    T, d = x.shape
+    E, d_ff, _ = Wg.q.shape
+    return MoeShape(T, d, E, top_k, d_ff, eps, _dt(x), MOE_BF16, _dt(out))
+
+
+@_current_device
+def forward_w4_workspace_bytes(x, Wg: W4Weights, out, top_k: int = 8, eps: float = 1e-5) -> int:
+    """Bytes of workspace ``moe_forward_w4`` needs for these tensors (queues nothing)."""
+    shp = _shape_w4(x, Wg, out, top_k, eps)
+    w = MoeWeightsW4()
+    w.group = Wg.group
+    n = ctypes.c_size_t(0)
+    _check("moe_forward_w4", _lib.moe_forward_w4(ctypes.byref(shp), ctypes.byref(w), None, None, None, None, None, None,
+                                                 ctypes.byref(n), None, _stream(x.device)))
+    return int(n.value)
+
+
+@_current_device
+def moe_forward_w4(x, gamma, W_r, b, Wg: W4Weights, Wu: W4Weights, Wd: W4Weights, out, top_k: int = 8,
+                   eps: float = 1e-5, topk_idx=None, topk_w=None, logits=None, ws=None, dev_status=None) -> None:
+    """out = x + MoE(RMSNorm(x)) with 4-bit experts."""
+    T, d = x.shape
+    E, d_ff, _ = Wg.q.shape
+    dev = x.device
+    _expect("out", out, (T, d), out.dtype, dev)
+    _expect("gamma", gamma, (d,), torch.float32, dev)
+    _expect("W_r", W_r, (E, d), torch.float32, dev)
+    _expect("b", b, (E,), torch.float32, dev)
+    for name, t, shape, dtype in (("topk_idx", topk_idx, (T, top_k), torch.int32),
+                                  ("topk_w", topk_w, (T, top_k), torch.float32),
+                                  ("logits", logits, (T, E), torch.float32)):
+        if t is not None:
+            _expect(name, t, shape, dtype, dev)
+    _status(dev_status, dev)
+    shp = _shape_w4(x, Wg, out, top_k, eps)
+    w = _w4_weights(gamma, W_r, b, Wg, Wu, Wd, E, d, d_ff, dev)
+    if ws is None:
+        ws = torch.empty(max(forward_w4_workspace_bytes(x, Wg, out, top_k, eps), 1), dtype=torch.uint8, device=dev)
+    n = ctypes.c_size_t(ws.numel() * ws.element_size())
+    _check("moe_forward_w4", _lib.moe_forward_w4(ctypes.byref(shp), ctypes.byref(w), _p(x), _p(out), _p(topk_idx),
+                                                 _p(topk_w), _p(logits), _p(ws), ctypes.byref(n), _p(dev_status),
+                                                 _stream(dev)))

@@ -620,4 +620,214 @@ moe_status_t moe_forward_fp8(const moe_shape_t* shape, const moe_weights_fp8_t* 
     return cuda_status(launch_combine(c, y, MOE_BF16, token_slot, wgt, x, xdt, T, d, k, out, shape->out_dtype));
 }
 
+// ----------------------------------------------------------------------------- 4-bit experts
+namespace {
+
+moe_status_t check_w4_group(int group) { return group == 32 || group == 64 || group == 128 ? MOE_OK : MOE_ERR_UNSUPPORTED; }
+
+moe_status_t check_w4_shape(int S, int E, int d, int d_ff, int group) {
+    if (S < 0 || E <= 0 || d <= 0 || d_ff <= 0) return MOE_ERR_INVALID_ARG;
+    if (E > MOE_MAX_EXPERTS || d % 32 != 0 || d_ff % 32 != 0 || d > MOE_W4_MAX_DIM || d_ff > MOE_W4_MAX_DIM)
+        return MOE_ERR_UNSUPPORTED;
+    return check_w4_group(group);
+}
+
+bool valid_w4(const moe_w4_t& w) { return w.q && w.s && aligned16(w.q) && aligned16(w.s) && aligned16(w.z); }
+W4 to_w4(const moe_w4_t& w) { return W4{w.q, static_cast<const uint16_t*>(w.s), w.z}; }
+bool valid_gate_up(const moe_w4_t& g, const moe_w4_t& u) { return valid_w4(g) && valid_w4(u) && !g.z == !u.z; }
+
+// the intermediates of the expert MLP of few picks: h as two bf16 terms, y in fp32, the combine's slot map
+struct PicksWs {
+    void* h;
+    float* y;
+    int32_t* slot;
+};
+PicksWs carve_picks(Carve& cv, int P, int d, int d_ff) {
+    PicksWs w;
+    w.h = cv.take((size_t)2 * P * d_ff * 2);
+    w.y = static_cast<float*>(cv.take((size_t)P * d * sizeof(float)));
+    w.slot = static_cast<int32_t*>(cv.take((size_t)P * sizeof(int32_t)));
+    return w;
+}
+
+moe_status_t run_picks(const Ctx& c, const void* v, const moe_weights_w4_t* w, const int32_t* idx, const float* wgt,
+                       const void* residual, moe_dtype_t r_dt, int T, int k, int E, int d, int d_ff, void* out,
+                       moe_dtype_t out_dt, const PicksWs& ws, int32_t* dev_status) {
+    moe_status_t st = cuda_status(launch_gate_up_w4_picks(c, v, to_w4(w->W_gate), to_w4(w->W_up), w->group, idx, T, k, E,
+                                                          d, d_ff, ws.h, ws.slot, dev_status));
+    if (st != MOE_OK) return st;
+    st = cuda_status(launch_down_w4_picks(c, ws.h, to_w4(w->W_down), w->group, idx, T, k, E, d, d_ff, ws.y, dev_status));
+    if (st != MOE_OK) return st;
+    return cuda_status(launch_combine(c, ws.y, MOE_F32, ws.slot, wgt, residual, r_dt, T, d, k, out, out_dt));
+}
+
+}  // namespace
+
+moe_status_t moe_quantize_w4(const void* x, moe_dtype_t dt, int32_t E, int64_t n, int32_t k, int32_t group, uint8_t* q,
+                             void* s, uint8_t* z, moe_stream_t stream) {
+    if (!valid_dt(dt) || E < 0 || n < 0 || k <= 0) return MOE_ERR_INVALID_ARG;
+    if (k % 32 != 0 || E > 65535 || n >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    moe_status_t st = check_w4_group(group);
+    if (st != MOE_OK || E == 0 || n == 0) return st;
+    if (!x || !q || !s || !aligned16(x) || !aligned16(q) || !aligned16(s) || !aligned16(z)) return MOE_ERR_INVALID_ARG;
+    Ctx c;
+    st = make_ctx(stream, c);
+    if (st != MOE_OK) return st;
+    return cuda_status(launch_quant_w4(c, x, dt, E, n, k, group, q, static_cast<uint16_t*>(s), z));
+}
+
+moe_status_t moe_dequantize_w4(const moe_w4_t* w, int32_t E, int64_t n, int32_t k, int32_t group, void* out,
+                               moe_dtype_t out_dt, moe_stream_t stream) {
+    if (!w || !valid_dt(out_dt) || E < 0 || n < 0 || k <= 0) return MOE_ERR_INVALID_ARG;
+    if (k % 32 != 0 || E > 65535 || n >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    moe_status_t st = check_w4_group(group);
+    if (st != MOE_OK || E == 0 || n == 0) return st;
+    if (!valid_w4(*w) || !out || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+    Ctx c;
+    st = make_ctx(stream, c);
+    if (st != MOE_OK) return st;
+    return cuda_status(launch_dequant_w4(c, w->q, static_cast<const uint16_t*>(w->s), w->z, E, n, k, group, out, out_dt));
+}
+
+moe_status_t moe_expert_gate_up_w4(const void* xp, const moe_w4_t* W_gate, const moe_w4_t* W_up, int32_t group,
+                                   const int32_t* counts, const int32_t* offsets, int32_t S, int32_t E, int32_t d,
+                                   int32_t d_ff, void* h, int32_t* dev_status, moe_stream_t stream) {
+    moe_status_t st = check_w4_shape(S, E, d, d_ff, group);
+    if (st != MOE_OK || S == 0) return st;
+    if (!xp || !W_gate || !W_up || !counts || !offsets || !h || !aligned16(xp) || !aligned16(h)) return MOE_ERR_INVALID_ARG;
+    if (!valid_gate_up(*W_gate, *W_up)) return MOE_ERR_INVALID_ARG;
+    Ctx c;
+    st = make_ctx(stream, c);
+    if (st != MOE_OK) return st;
+    return cuda_status(
+        launch_gate_up_w4(c, xp, to_w4(*W_gate), to_w4(*W_up), group, counts, offsets, S, E, d, d_ff, h, dev_status));
+}
+
+moe_status_t moe_expert_down_w4(const void* h, const moe_w4_t* W_down, int32_t group, const int32_t* counts,
+                                const int32_t* offsets, int32_t S, int32_t E, int32_t d, int32_t d_ff, void* y,
+                                int32_t* dev_status, moe_stream_t stream) {
+    moe_status_t st = check_w4_shape(S, E, d, d_ff, group);
+    if (st != MOE_OK || S == 0) return st;
+    if (!h || !W_down || !counts || !offsets || !y || !aligned16(h) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+    if (!valid_w4(*W_down)) return MOE_ERR_INVALID_ARG;
+    Ctx c;
+    st = make_ctx(stream, c);
+    if (st != MOE_OK) return st;
+    return cuda_status(launch_down_w4(c, h, to_w4(*W_down), group, counts, offsets, S, E, d, d_ff, y, dev_status));
+}
+
+moe_status_t moe_grouped_swiglu_w4(const void* xp, const moe_weights_w4_t* w, const int32_t* counts,
+                                   const int32_t* offsets, int32_t S, int32_t E, int32_t d, int32_t d_ff, void* h,
+                                   void* y, int32_t* dev_status, moe_stream_t stream) {
+    if (!w) return MOE_ERR_INVALID_ARG;
+    moe_status_t st = check_w4_shape(S, E, d, d_ff, w->group);
+    if (st != MOE_OK || S == 0) return st;
+    if (!valid_w4(w->W_down) || !y || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+    st = moe_expert_gate_up_w4(xp, &w->W_gate, &w->W_up, w->group, counts, offsets, S, E, d, d_ff, h, dev_status, stream);
+    if (st != MOE_OK) return st;
+    return moe_expert_down_w4(h, &w->W_down, w->group, counts, offsets, S, E, d, d_ff, y, dev_status, stream);
+}
+
+moe_status_t moe_picks_swiglu_w4(const void* v, const moe_weights_w4_t* w, const int32_t* topk_idx, const float* topk_w,
+                                 const void* residual, moe_dtype_t r_dt, int32_t T, int32_t k, int32_t E, int32_t d,
+                                 int32_t d_ff, void* out, moe_dtype_t out_dt, void* ws, size_t* ws_bytes,
+                                 int32_t* dev_status, moe_stream_t stream) {
+    if (!w || T < 0 || k <= 0 || !valid_dt(r_dt) || !valid_dt(out_dt)) return MOE_ERR_INVALID_ARG;
+    moe_status_t st = check_w4_shape(T, E, d, d_ff, w->group);
+    if (st != MOE_OK) return st;
+    if (k > MOE_MAX_TOP_K || (int64_t)T * k > MOE_W4_MAX_PICKS) return MOE_ERR_UNSUPPORTED;
+    Carve cv(ws);
+    const PicksWs pw = carve_picks(cv, T * k, d, d_ff);
+    bool query = false;
+    st = check_ws(ws, ws_bytes, cv.off, &query);
+    if (st != MOE_OK || query || T == 0) return st;
+    if (!v || !topk_idx || !topk_w || !residual || !out || !aligned16(v) || !aligned16(residual) || !aligned16(out))
+        return MOE_ERR_INVALID_ARG;
+    if (!valid_gate_up(w->W_gate, w->W_up) || !valid_w4(w->W_down)) return MOE_ERR_INVALID_ARG;
+    Ctx c;
+    st = make_ctx(stream, c);
+    if (st != MOE_OK) return st;
+    return run_picks(c, v, w, topk_idx, topk_w, residual, r_dt, T, k, E, d, d_ff, out, out_dt, pw, dev_status);
+}
+
+moe_status_t moe_forward_w4(const moe_shape_t* shape, const moe_weights_w4_t* w, const void* x, void* out,
+                            int32_t* topk_idx, float* topk_w, float* logits, void* ws, size_t* ws_bytes,
+                            int32_t* dev_status, moe_stream_t stream) {
+    if (!shape || !w || !ws_bytes) return MOE_ERR_INVALID_ARG;
+    const int T = shape->T, d = shape->d, E = shape->E, k = shape->top_k, d_ff = shape->d_ff;
+    if (!valid_dt(shape->x_dtype) || !valid_dt(shape->out_dtype)) return MOE_ERR_INVALID_ARG;
+    moe_status_t st = check_router_shape(T, d, E, k);
+    if (st != MOE_OK) return st;
+    if ((int64_t)T * k > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
+    const int S = T * k;
+    st = check_w4_shape(S, E, d, d_ff, w->group);
+    if (st != MOE_OK) return st;
+    Ctx c;
+    st = make_ctx(stream, c);
+    if (st != MOE_OK) return st;
+    const RouterPlan plan = plan_router(T, d, E, c.num_sms);
+    const bool picks = w4_use_picks(T, k, E);
+
+    Carve cv(ws);
+    void* v = cv.take((size_t)T * d * 2);
+    float* rstd = static_cast<float*>(cv.take((size_t)T * sizeof(float)));
+    float* partial = static_cast<float*>(cv.take(plan.partial_bytes));
+    float* wsplit = static_cast<float*>(cv.take(plan.wsplit_bytes));
+    int32_t* idx_ws = static_cast<int32_t*>(cv.take((size_t)S * sizeof(int32_t)));
+    float* wgt_ws = static_cast<float*>(cv.take((size_t)S * sizeof(float)));
+    int32_t* idx = topk_idx ? topk_idx : idx_ws;
+    float* wgt = topk_w ? topk_w : wgt_ws;
+    PicksWs pw{};
+    int32_t *hist = nullptr, *counts = nullptr, *offsets = nullptr, *slot_token = nullptr, *token_slot = nullptr;
+    void *h = nullptr, *y = nullptr;
+    if (picks) {
+        pw = carve_picks(cv, S, d, d_ff);
+    } else {
+        hist = static_cast<int32_t*>(cv.take(permute_ws_bytes(T, E)));
+        counts = static_cast<int32_t*>(cv.take((size_t)E * sizeof(int32_t)));
+        offsets = static_cast<int32_t*>(cv.take((size_t)(E + 1) * sizeof(int32_t)));
+        slot_token = static_cast<int32_t*>(cv.take((size_t)S * sizeof(int32_t)));
+        token_slot = static_cast<int32_t*>(cv.take((size_t)S * sizeof(int32_t)));
+        h = cv.take((size_t)S * d_ff * 2);
+        y = cv.take((size_t)S * d * 2);
+    }
+    bool query = false;
+    st = check_ws(ws, ws_bytes, cv.off, &query);
+    if (st != MOE_OK || query) return st;
+
+    if (T > 0) {
+        if (!x || !out || !w->gamma || !w->W_r || !w->b) return MOE_ERR_INVALID_ARG;
+        if (!aligned16(x) || !aligned16(out) || !aligned16(w->gamma) || !aligned16(w->W_r)) return MOE_ERR_INVALID_ARG;
+        if (!valid_gate_up(w->W_gate, w->W_up) || !valid_w4(w->W_down)) return MOE_ERR_INVALID_ARG;
+    }
+    if (dev_status) {
+        st = cuda_status(cudaMemsetAsync(dev_status, 0, sizeof(int32_t), c.stream));
+        if (st != MOE_OK) return st;
+    }
+    if (T == 0) return MOE_OK;
+    const int xdt = shape->x_dtype;
+    // 1-2. RMSNorm (rows rounded to bf16 for the experts, 1/rms for the router) and the router, as in moe_forward
+    st = cuda_status(launch_rmsnorm(c, x, xdt, w->gamma, T, d, shape->eps, v, MOE_BF16, rstd));
+    if (st != MOE_OK) return st;
+    st = cuda_status(
+        launch_router_logits(c, plan, x, xdt, rstd, w->gamma, w->W_r, T, d, E, partial, wsplit, dev_status));
+    if (st != MOE_OK) return st;
+    st = cuda_status(launch_router_topk(c, plan, partial, w->b, T, E, k, idx, wgt, logits, nullptr));
+    if (st != MOE_OK) return st;
+    if (picks)
+        return run_picks(c, v, w, idx, wgt, x, shape->x_dtype, T, k, E, d, d_ff, out, shape->out_dtype, pw, dev_status);
+    // 3. permutation maps only: gate/up reads the rows in place
+    st = cuda_status(launch_permute(c, nullptr, MOE_BF16, idx, T, d, E, k, counts, offsets, slot_token, token_slot,
+                                    nullptr, hist, dev_status));
+    if (st != MOE_OK) return st;
+    // 4. 4-bit SwiGLU MLP
+    st = cuda_status(launch_gate_up_w4(c, v, to_w4(w->W_gate), to_w4(w->W_up), w->group, counts, offsets, S, E, d, d_ff, h,
+                                       dev_status, slot_token, T));
+    if (st != MOE_OK) return st;
+    st = cuda_status(launch_down_w4(c, h, to_w4(w->W_down), w->group, counts, offsets, S, E, d, d_ff, y, dev_status));
+    if (st != MOE_OK) return st;
+    // 5. weighted un-permute + residual
+    return cuda_status(launch_combine(c, y, MOE_BF16, token_slot, wgt, x, xdt, T, d, k, out, shape->out_dtype));
+}
+
 }  // extern "C"

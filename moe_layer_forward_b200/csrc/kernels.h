@@ -145,6 +145,33 @@ cudaError_t launch_gate_up_f32(const Ctx& c, const float* xp, const float* Wg, c
 cudaError_t launch_down_f32(const Ctx& c, const float* h, const float* Wd, const int32_t* counts,
                             const int32_t* offsets, int S, int E, int d, int d_ff, float* y, int32_t* status);
 
+// ---- 4-bit experts: codes q [E][n][k / 2], scales s (bf16) and zero points z (null: 8) [E][G][n] of a matrix
+// (quant_w4.cu: the format, quantisation and its inverse; expert_w4.cu: few rows per expert)
+struct W4 {
+    const uint8_t* q;
+    const uint16_t* s;
+    const uint8_t* z;
+};
+cudaError_t launch_quant_w4(const Ctx& c, const void* x, int dt, int E, int64_t n, int k, int group, uint8_t* q,
+                            uint16_t* s, uint8_t* z);
+cudaError_t launch_dequant_w4(const Ctx& c, const uint8_t* q, const uint16_t* s, const uint8_t* z, int E, int64_t n, int k,
+                              int group, void* out, int dt);
+// from the router's picks (T k <= 256): h keeps two bf16 terms [2][T k][d_ff], y [T k][d] is fp32; slot gets the
+// identity map for the combine (-1 for a bad id)
+cudaError_t launch_gate_up_w4_picks(const Ctx& c, const void* v, const W4& Wg, const W4& Wu, int group,
+                                    const int32_t* idx, int T, int k, int E, int d, int d_ff, void* h, int32_t* slot,
+                                    int32_t* status);
+cudaError_t launch_down_w4_picks(const Ctx& c, const void* h, const W4& Wd, int group, const int32_t* idx, int T, int k,
+                                 int E, int d, int d_ff, float* y, int32_t* status);
+// moe_forward_w4 takes that form: few tokens, so that experts have a row or two each
+inline bool w4_use_picks(int T, int k, int E) { return T * k <= 128 && (T <= 8 || T * k <= 2 * E); }
+// expert-contiguous rows; gather (gate/up): slot i reads row gather[i] of act_rows rows
+cudaError_t launch_gate_up_w4(const Ctx& c, const void* xp, const W4& Wg, const W4& Wu, int group, const int32_t* counts,
+                              const int32_t* offsets, int S, int E, int d, int d_ff, void* h, int32_t* status,
+                              const int32_t* gather = nullptr, int act_rows = 0);
+cudaError_t launch_down_w4(const Ctx& c, const void* h, const W4& Wd, int group, const int32_t* counts,
+                           const int32_t* offsets, int S, int E, int d, int d_ff, void* y, int32_t* status);
+
 // ---- step 5: weighted un-permute + residual (combine.cu)
 cudaError_t launch_combine(const Ctx& c, const void* y, int y_dt, const int32_t* token_slot, const float* w,
                            const void* res, int r_dt, int T, int d, int k, void* out, int out_dt);

@@ -1,0 +1,120 @@
+"""4-bit experts without a GPU: the packed layout, and what the C ABI refuses on the host."""
+import ctypes
+
+import pytest
+import torch
+
+import _w4_ref as ref
+from test_abi import INVALID, OK, UNSUPPORTED, WORKSPACE, lib  # noqa: F401 (fixture)
+
+V, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+P = 0x10000  # an aligned address that no refused call touches
+
+
+class W4(ctypes.Structure):
+    _fields_ = [("q", V), ("s", V), ("z", V)]
+
+
+class Weights(ctypes.Structure):
+    _fields_ = [("gamma", V), ("W_r", V), ("b", V), ("W_gate", W4), ("W_up", W4), ("W_down", W4), ("group", i32)]
+
+
+class Shape(ctypes.Structure):
+    _fields_ = [(n, i32) for n in ("T", "d", "E", "top_k", "d_ff")] + [("eps", ctypes.c_float)] + [
+        (n, ctypes.c_int) for n in ("x_dtype", "w_dtype", "out_dtype")]
+
+
+def full(group=128, z=None):
+    w = W4(P, P, z)
+    return Weights(P, P, P, w, w, w, group)
+
+
+def test_packed_layout():
+    import moe_layer_forward_b200 as moe
+
+    codes = torch.randint(0, 16, (3, 5, 96))
+    q = moe.pack_w4(codes.to(torch.uint8))
+    assert torch.equal(q, ref.pack(codes)) and torch.equal(moe.unpack_w4(q).long(), codes)
+    one = torch.zeros((1, 8), dtype=torch.uint8)
+    for j in range(8):
+        one.zero_()
+        one[0, j] = 15
+        word = int.from_bytes(bytes(moe.pack_w4(one)[0].tolist()), "little")
+        assert word == 15 << (4 * (j // 2 + 4 * (j % 2)))
+
+
+@pytest.mark.parametrize("group", [0, 16, 256, -32, 96])
+def test_group_sizes_refused(lib, group):  # noqa: F811
+    lib.moe_quantize_w4.argtypes = [V, i32, i32, i64, i32, i32, V, V, V, V]
+    assert lib.moe_quantize_w4(P, 0, 1, 8, 64, group, P, P, None, None) == UNSUPPORTED
+    lib.moe_dequantize_w4.argtypes = [V, i32, i64, i32, i32, V, i32, V]
+    assert lib.moe_dequantize_w4(ctypes.byref(W4(P, P, None)), 1, 8, 64, group, P, 0, None) == UNSUPPORTED
+    lib.moe_expert_down_w4.argtypes = [V, V, i32, V, V, i32, i32, i32, i32, V, V, V]
+    assert lib.moe_expert_down_w4(P, ctypes.byref(W4(P, P, None)), group, P, P, 4, 2, 64, 64, P, None, None) == UNSUPPORTED
+
+
+def test_quantize_refusals(lib):  # noqa: F811
+    q = lib.moe_quantize_w4
+    q.argtypes = [V, i32, i32, i64, i32, i32, V, V, V, V]
+    assert q(P, 2, 1, 8, 64, 32, P, P, None, None) == INVALID  # dtype
+    assert q(P, 0, -1, 8, 64, 32, P, P, None, None) == INVALID
+    assert q(P, 0, 1, 8, 0, 32, P, P, None, None) == INVALID
+    assert q(P, 0, 1, 8, 48, 32, P, P, None, None) == UNSUPPORTED
+    assert q(P, 0, 70000, 8, 64, 32, P, P, None, None) == UNSUPPORTED
+    assert q(None, 0, 1, 8, 64, 32, P, P, None, None) == INVALID
+    assert q(P + 8, 0, 1, 8, 64, 32, P, P, None, None) == INVALID
+    assert q(P, 0, 1, 8, 64, 32, P + 4, P, None, None) == INVALID
+    assert q(P, 0, 0, 8, 64, 32, P, P, None, None) == OK
+    assert q(P, 0, 1, 0, 64, 32, P, P, None, None) == OK
+
+
+def test_grouped_refusals(lib):  # noqa: F811
+    f = lib.moe_expert_gate_up_w4
+    f.argtypes = [V, V, V, i32, V, V, i32, i32, i32, i32, V, V, V]
+    w, wz, bad = W4(P, P, None), W4(P, P, P), W4(P + 8, P, None)
+    r = ctypes.byref
+
+    def call(xp=P, g=w, u=w, group=32, S=4, E=2, d=64, d_ff=96, h=P, counts=P):
+        return f(xp, r(g), r(u), group, counts, P, S, E, d, d_ff, h, None, None)
+
+    assert call(d=48) == UNSUPPORTED and call(d_ff=40) == UNSUPPORTED and call(E=257) == UNSUPPORTED
+    assert call(d=16416) == UNSUPPORTED and call(d_ff=32768) == UNSUPPORTED
+    assert call(S=-1) == INVALID and call(E=0) == INVALID and call(d=-64) == INVALID
+    assert call(xp=None) == INVALID and call(h=P + 2) == INVALID and call(counts=None) == INVALID
+    assert call(g=bad) == INVALID and call(g=w, u=wz) == INVALID and call(g=W4(P, None, None)) == INVALID
+    assert call(S=0) == OK
+    g = lib.moe_grouped_swiglu_w4
+    g.argtypes = [V, V, V, V, i32, i32, i32, i32, V, V, V, V]
+    assert g(P, None, P, P, 4, 2, 64, 64, P, P, None, None) == INVALID
+    assert g(P, r(full(33)), P, P, 4, 2, 64, 64, P, P, None, None) == UNSUPPORTED
+    assert g(P, r(full()), P, P, 4, 2, 64, 64, P, None, None, None) == INVALID
+
+
+def test_picks_and_layer_refusals(lib):  # noqa: F811
+    f = lib.moe_picks_swiglu_w4
+    f.argtypes = [V, V, V, V, V, i32, i32, i32, i32, i32, i32, V, i32, V, V, V, V]
+    n = ctypes.c_size_t(0)
+    r = ctypes.byref
+
+    def call(w=None, T=4, k=2, E=8, d=64, d_ff=96, ws=None, v=P, r_dt=0, nb=n):
+        return f(v, r(w or full()), P, P, P, r_dt, T, k, E, d, d_ff, P, 1, ws, r(nb) if nb is not None else None, None,
+                 None)
+
+    assert call() == OK and n.value >= 4 * 2 * (96 * 4 + 64 * 4)  # the query
+    assert call(ws=P, nb=ctypes.c_size_t(16)) == WORKSPACE
+    assert call(ws=P + 16, nb=ctypes.c_size_t(1 << 20)) == INVALID  # not 256-byte aligned
+    assert call(nb=None) == INVALID
+    assert call(T=129) == UNSUPPORTED and call(T=257, k=1) == UNSUPPORTED and call(k=9, T=1) == UNSUPPORTED
+    assert call(T=-1) == INVALID and call(k=0) == INVALID and call(r_dt=5) == INVALID
+    assert call(ws=P, nb=ctypes.c_size_t(1 << 20), v=None) == INVALID
+    assert call(T=0, ws=P, nb=ctypes.c_size_t(1 << 20)) == OK
+    g = lib.moe_forward_w4
+    g.argtypes = [V, V, V, V, V, V, V, V, V, V, V]
+    s = Shape(4, 64, 8, 2, 96, 1e-5, 0, 1, 0)
+    for field, value, want in (("d", 72, UNSUPPORTED), ("d_ff", 100, UNSUPPORTED), ("top_k", 9, UNSUPPORTED),
+                               ("E", 300, UNSUPPORTED), ("T", -1, INVALID), ("x_dtype", 7, INVALID)):
+        bad = Shape(*[getattr(s, n) for n, _ in Shape._fields_])
+        setattr(bad, field, value)
+        assert g(r(bad), r(full()), P, P, None, None, None, None, r(n), None, None) == want
+    assert g(None, r(full()), P, P, None, None, None, None, r(n), None, None) == INVALID
+    assert g(r(s), r(full(7)), P, P, None, None, None, None, r(n), None, None) == UNSUPPORTED
