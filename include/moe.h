@@ -103,8 +103,9 @@ typedef struct {
  * and zero point serve `group` consecutive columns of a row and G = ceil(k / group):
  *   w[e][n][j] = (code(e, n, j) - z[e][j / group][n]) * s[e][j / group][n]
  * Eight columns of a row are one little-endian 32-bit word: nibble i (0..3) holds column 2 i, nibble 4 + i
- * column 2 i + 1.  Where (code - z) * s needs more than bf16's 8 significant bits it is rounded to bf16 (to
- * nearest even) before the products; with moe_quantize_w4's scales it never does. */
+ * column 2 i + 1.  Where (code - z) * s needs more than bf16's 8 significant bits, a product with many rows
+ * takes it rounded to bf16 (to nearest even), one with few rows as it is; with moe_quantize_w4's scales both are
+ * the same number. */
 typedef struct {
     const uint8_t* q;
     const void* s;
@@ -388,7 +389,7 @@ moe_status_t moe_quantize_w4(const void* x, moe_dtype_t dt, int32_t E, int64_t n
                              void* s, uint8_t* z, moe_stream_t stream);
 
 /* The weights that codes, scales and zero points stand for: out [E][n][k] (out_dt) = (code - z) * s, rounded to
- * out_dt.  With MOE_BF16 these are the weights of the products below. */
+ * out_dt. */
 moe_status_t moe_dequantize_w4(const moe_w4_t* w, int32_t E, int64_t n, int32_t k, int32_t group, void* out,
                                moe_dtype_t out_dt, moe_stream_t stream);
 

@@ -636,15 +636,15 @@ bool valid_w4(const moe_w4_t& w) { return w.q && w.s && aligned16(w.q) && aligne
 W4 to_w4(const moe_w4_t& w) { return W4{w.q, static_cast<const uint16_t*>(w.s), w.z}; }
 bool valid_gate_up(const moe_w4_t& g, const moe_w4_t& u) { return valid_w4(g) && valid_w4(u) && !g.z == !u.z; }
 
-// the intermediates of the expert MLP of few picks: h as two bf16 terms, y in fp32, the combine's slot map
+// the intermediates of the expert MLP of few picks: h and y in fp32, the combine's slot map
 struct PicksWs {
-    void* h;
+    float* h;
     float* y;
     int32_t* slot;
 };
 PicksWs carve_picks(Carve& cv, int P, int d, int d_ff) {
     PicksWs w;
-    w.h = cv.take((size_t)2 * P * d_ff * 2);
+    w.h = static_cast<float*>(cv.take((size_t)P * d_ff * sizeof(float)));
     w.y = static_cast<float*>(cv.take((size_t)P * d * sizeof(float)));
     w.slot = static_cast<int32_t*>(cv.take((size_t)P * sizeof(int32_t)));
     return w;
@@ -653,10 +653,12 @@ PicksWs carve_picks(Carve& cv, int P, int d, int d_ff) {
 moe_status_t run_picks(const Ctx& c, const void* v, const moe_weights_w4_t* w, const int32_t* idx, const float* wgt,
                        const void* residual, moe_dtype_t r_dt, int T, int k, int E, int d, int d_ff, void* out,
                        moe_dtype_t out_dt, const PicksWs& ws, int32_t* dev_status) {
+    const bool exact = out_dt == MOE_F32;
     moe_status_t st = cuda_status(launch_gate_up_w4_picks(c, v, to_w4(w->W_gate), to_w4(w->W_up), w->group, idx, T, k, E,
-                                                          d, d_ff, ws.h, ws.slot, dev_status));
+                                                          d, d_ff, ws.h, ws.slot, exact, dev_status));
     if (st != MOE_OK) return st;
-    st = cuda_status(launch_down_w4_picks(c, ws.h, to_w4(w->W_down), w->group, idx, T, k, E, d, d_ff, ws.y, dev_status));
+    st = cuda_status(launch_down_w4_picks(c, ws.h, to_w4(w->W_down), w->group, idx, T, k, E, d, d_ff, ws.y,
+                                          exact, dev_status));
     if (st != MOE_OK) return st;
     return cuda_status(launch_combine(c, ws.y, MOE_F32, ws.slot, wgt, residual, r_dt, T, d, k, out, out_dt));
 }

@@ -1,46 +1,56 @@
 // 4-bit experts for few rows per expert: a stream of weights past a handful of token rows.
 //
-//   gate/up   h[r] = SiLU(Wg x[r]) * (Wu x[r])       down   y[r] = Wd h[r],      w = bf16((q - z) * s)
+//   gate/up   h[r] = SiLU(Wg x[r]) * (Wu x[r])       down   y[r] = Wd h[r],      w = (q - z) * s
 //
 // Two forms of the same kernel:
 //   segments  rows are expert-contiguous (counts, offsets as written by the permutation), optionally read
 //             through a slot -> token map
 //   picks     straight from the router's picks topk_idx [T][k] (T k <= 256): every CTA sorts the picks by
-//             expert itself, so a token needs no permutation and no permuted copy.  h is kept as two bf16
-//             terms (h = hi + lo to 16 bits), which ride as two sets of columns of the same products, and the
-//             outputs are fp32: the form for single tokens loses nothing between the router and the output.
+//             expert itself, so a token needs no permutation and no permuted copy.  h and y are fp32: the form
+//             for single tokens loses nothing between the router and the output.
 //
 // What bounds it: the weights' bytes.  At 6.5 TB/s each SM has to take 23 bytes, 46 weights, per clock, so every
-// step below is counted in instructions per weight.  A CUDA-core product of one row would need an FMA per
-// weight on top of the unpacking and could not keep up; mma.sync m16n8k16 takes the unpacked weights straight
-// from registers as its A operand (16 weight rows) with up to 8 token rows as B.  The wide tensor cores read
-// their operands from shared or tensor memory; that round trip pays only for many rows (expert_w4_tc.cu).
+// step is counted in instructions per weight.  Unpacking to bf16 and scaling there takes 2 per weight and left
+// the stream issue-bound at a quarter of the bandwidth (gate/up of 128 tokens, 8 rows per expert: 486 us).
+//
+// The products therefore run on the codes as they are: masking a word's low and its high nibbles gives eight
+// unsigned bytes in three instructions, and mma.sync m16n8k32 on bytes (32-bit sums, exact) takes them straight
+// from registers at twice the multiply-adds of the bf16 form (measured 1950 against 990 per clock and SM; the E4M3
+// form is no instruction of its own here: it converts both operands first).  The wide tensor cores would want
+// the weights in shared or tensor memory, a round trip that pays only for many rows (expert_w4_tc.cu).
+//
+// The token rows are the operand that is split: per group of columns, a power of two c takes the largest
+// magnitude to 2 or 3 signed bytes, X = rint(x c) = 256 x1 + x0 (or 65536 x2 + 256 x1 + x0), and every byte is a
+// set of columns of the product.  Two bytes round a group's rows to 2^-15 of its largest value, a hundredth
+// of what rounding the output to bf16 does; three, for fp32 outputs, to 2^-23.  Scale and zero point come
+// after the group's integer sum P:  y += s / c * (P - z * sum X).
 //
 // Layout.  A unit is 16 weight rows over the whole K: 8 gate and the 8 up rows of the same features (then the
 // accumulators of a thread hold g and u of the same element), or 16 rows of down.  Warps are independent: each
-// streams its units through a ring of its own (cp.async, 256 columns a stage, 16-byte pieces swizzled by row),
-// with no barrier between warps.  Thread (g, t) = (lane / 4, lane % 4) takes word t of every 32-column piece of
-// rows g and g + 8: K inside a piece is permuted alike in A and B, so a word's four pairs feed two MMAs and
-// the B operand is 16 consecutive bytes of token row g.  The units of all experts form one list, cut evenly
-// over the CTAs; a CTA stages the token rows of the experts its share touches in shared memory, as many
-// experts at a time as fit.
+// streams its units through a ring of its own (cp.async, 256 columns a stage), with no barrier between warps.
+// Thread (g, t) = (lane / 4, lane % 4) takes GP = group / 32 consecutive words of every group of rows g and
+// g + 8, word t GP + i in MMA i: any order of K will do as long as A and B agree, and the token rows are stored
+// in the order that masking gives (columns 0 4 1 5 | 2 6 3 7 of a word).  16-byte pieces are swizzled with the
+// row times GP so that those reads meet no bank twice.  The units of all experts form one list, cut evenly over
+// the CTAs; a CTA stages the token rows of the experts its share touches, as many experts at a time as fit.
 #include "common.cuh"
 #include "kernels.h"
 
 namespace moe {
 namespace w4s {
 
-constexpr int kWarps = 16;
+constexpr int kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kStages = 3;
 constexpr int kStageCols = 256;
 constexpr int kCodeBytes = 16 * (kStageCols / 2);            // 16 rows x 128 bytes
 constexpr int kScaleOff = kCodeBytes;                        // [group][16 rows] bf16
 constexpr int kZeroOff = kScaleOff + (kStageCols / 32) * 32; // [group][16 rows] u8
 constexpr int kStageBytes = kZeroOff + (kStageCols / 32) * 16;
-constexpr int kStages = 4;
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kSmemLimit = 232448;
 constexpr int kMaxPicks = 256;
+static_assert(kThreads >= kMaxPicks, "a thread per pick");
 
 struct Args {
     const uint8_t* q0;  // gate (rows 0..7 of a unit) or down
@@ -49,7 +59,7 @@ struct Args {
     const uint16_t* s1;
     const uint8_t* z0;
     const uint8_t* z1;
-    const uint16_t* x;  // token rows bf16 [rows][K]; picks / down: the hi rows, the lo rows after them
+    const void* x;           // token rows [rows][K]: bf16, or (picks / down) fp32
     const int32_t* gather;   // segments: slot i reads row gather[i] of act_rows rows
     const int32_t* counts;   // segments
     const int32_t* offsets;  // segments
@@ -57,11 +67,11 @@ struct Args {
     int P;                   // picks: T k;  segments: rows of the buffers
     int top_k;
     int act_rows;
-    int E, K, n_out, G, group;
-    int chunk_rows;  // rows of one pass over an expert's weights (<= 8 NT; 8 with two terms)
+    int E, K, n_out, G;
+    int chunk_rows;  // rows of one pass over an expert's weights (<= 8 NT)
     int xcap;        // token rows that fit in shared memory
     int x_stride;    // bytes of a staged row
-    void* out;       // gate/up: h bf16 (picks: hi rows, then lo rows);  down: y (segments bf16, picks fp32)
+    void* out;       // gate/up: h (segments bf16, picks fp32);  down: y (segments bf16, picks fp32)
     int32_t* slot_out;  // picks, gate/up: identity slot map for the combine, -1 for a bad id
     int32_t* status;
 };
@@ -76,6 +86,7 @@ struct Aux {
     int b_n;
     int be[32], bfirst[32], bn[32], brow[32];
 };
+constexpr int kAuxBytes = (sizeof(Aux) + 127) & ~127;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
@@ -87,57 +98,46 @@ __device__ __forceinline__ void cp8(uint32_t dst, const void* src) {
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ void lds128(uint32_t a, uint32_t (&v)[4]) {
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a));
-}
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+__device__ __forceinline__ void mma(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+          "l"(*reinterpret_cast<uint64_t*>(&c)));
+    return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+    return *reinterpret_cast<float2*>(&r);
+}
 
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-// four bf16 pairs of a word: 0x4300 | q is 128 + q, minus 128 + z exactly, times s with one rounding (none with
-// the quantiser's scales)
-__device__ __forceinline__ void unpack(uint32_t w, uint32_t zz, uint32_t ss, uint32_t (&p)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = mul2(sub2(((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u, zz), ss);
+// four signed bytes, lowest first, of the low bytes of four integers
+__device__ __forceinline__ uint32_t bytes4(int a, int b, int c, int d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// NT: column sets of 8 token rows.  PICKS: the form above.  For picks / down (TERMS) set 0 is hi, set 1 lo.
-template <bool SWIGLU, bool PICKS, int NT, bool ZERO>
+// NT: column sets of 8 token rows.  PICKS: the form above.  TM: bytes of a token row's value.  GP: 32-column
+// pieces of a group.
+template <bool SWIGLU, bool PICKS, int NT, int TM, int GP, bool ZERO>
 __global__ void __launch_bounds__(kThreads, 1) stream_w4_kernel(const Args p) {
-    constexpr bool TERMS = PICKS && !SWIGLU;
-    static_assert(!TERMS || NT == 2, "hi and lo columns");
-    constexpr int XR = TERMS ? 2 : 1;  // staged rows per token row
+    constexpr bool F32X = PICKS && !SWIGLU;  // token rows are fp32
+    constexpr int GROUP = 32 * GP;
+    constexpr int NG = kStageCols / GROUP;  // groups of a stage
     extern __shared__ __align__(128) uint8_t smem[];
     Aux& aux = *reinterpret_cast<Aux*>(smem + kRingBytes);
-    uint8_t* xs = smem + kRingBytes + ((sizeof(Aux) + 127) & ~size_t(127));
+    // per (group, row): 1 / c, and the sum of X (an integer with two bytes, fp32 with three)
+    float2* meta = reinterpret_cast<float2*>(smem + kRingBytes + kAuxBytes);
+    const int meta_rows = (p.xcap + 8 * NT + 1) & ~1;
+    uint8_t* xs = smem + kRingBytes + kAuxBytes + p.G * meta_rows * (int)sizeof(float2);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int E = p.E;
 
@@ -216,10 +216,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_w4_kernel(const Args p) {
     const int64_t u_begin = total * blockIdx.x / gridDim.x, u_end = total * (blockIdx.x + 1) / gridDim.x;
     const int nstage = (p.K + kStageCols - 1) / kStageCols;
     const int pieces = p.K / 32;  // 32-column pieces of a row
-    const int NG = kStageCols / p.group;
-    const int gp = p.group / 32;  // pieces of a group
+    const int KP = p.G * GROUP;   // columns of a staged row: zeros past K
     const uint32_t ring = smem_addr(smem) + warp * kStages * kStageBytes;
-    const uint32_t xbase = smem_addr(xs);
     const int g = lane >> 2, t = lane & 3;
 
     // expert and first row of chunk v
@@ -233,26 +231,6 @@ __global__ void __launch_bounds__(kThreads, 1) stream_w4_kernel(const Args p) {
         first = (v - aux.vstart[e]) * p.chunk_rows;
         n = min(p.chunk_rows, aux.cnt[e] - first);
     };
-    // the ring's copies of one stage of unit (e, un)
-    auto issue = [&](int e, int un, int st, int slot) {
-        const uint32_t dst = ring + slot * kStageBytes;
-        const int64_t half_row = (int64_t)e * p.n_out + un * UROWS;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int i = j * 32 + lane, r = i >> 3, c = i & 7;
-            const int64_t row = half_row + (SWIGLU ? (r & 7) : r);
-            const uint8_t* src = (SWIGLU && r >= 8 ? p.q1 : p.q0) + row * (p.K / 2) + st * (kStageCols / 2) + c * 16;
-            if (st * 8 + c < pieces) cp16(dst + r * 128 + ((c ^ (r & 7)) << 4), src);
-        }
-        if (lane < 2 * NG) {
-            const int gr = st * NG + (lane >> 1), h = lane & 1;
-            if (gr < p.G) {
-                const int64_t at = ((int64_t)e * p.G + gr) * p.n_out + un * UROWS + (SWIGLU ? 0 : 8 * h);
-                cp16(dst + kScaleOff + lane * 16, (SWIGLU && h ? p.s1 : p.s0) + at);
-                if (ZERO) cp8(dst + kZeroOff + lane * 8, (SWIGLU && h ? p.z1 : p.z0) + at);
-            }
-        }
-    };
 
     for (int64_t b0 = u_begin; b0 < u_end;) {
         // ---- a batch: the chunks from the current one on whose rows fit together (32 at most)
@@ -263,7 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_w4_kernel(const Args p) {
             int e = 0, first = 0, n = 0;
             const bool in = v < aux.vstart[E] && (int64_t)v * nu < u_end;
             if (in) find(v, e, first, n);
-            int incl = n * XR;
+            const int even = (n + 1) & ~1;  // chunks start at even rows: two rows' meta is one read
+            int incl = even;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int m = __shfl_up_sync(0xffffffffu, incl, o);
@@ -272,8 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_w4_kernel(const Args p) {
             aux.be[lane] = e;
             aux.bfirst[lane] = first;
             aux.bn[lane] = n;
-            aux.brow[lane] = incl - n * XR;
-            const uint32_t fit = __ballot_sync(0xffffffffu, in && incl <= p.xcap);
+            aux.brow[lane] = incl - even;
+            const uint32_t fit = __ballot_sync(0xffffffffu, in && incl - even + n <= p.xcap);
             if (lane == 0) aux.b_n = __popc(fit);  // a prefix of the lanes; one chunk always fits
         }
         __syncthreads();
@@ -281,38 +260,40 @@ __global__ void __launch_bounds__(kThreads, 1) stream_w4_kernel(const Args p) {
         const int base_u = (int)(b0 - (int64_t)v0 * nu);  // units are counted from chunk v0's first
         const int end_u = (int)(min(u_end, (int64_t)(v0 + nv) * nu) - (int64_t)v0 * nu);
 
-        // ---- stage its token rows (asynchronously), then start this warp's weights
-        const int all_rows = aux.brow[nv - 1] + aux.bn[nv - 1] * XR;
-        for (int r = warp, ci = 0; r < all_rows; r += kWarps) {
-            while (ci + 1 < nv && aux.brow[ci + 1] <= r) ++ci;
-            const int n = aux.bn[ci], rr = r - aux.brow[ci];
-            const int at = aux.off[aux.be[ci]] + aux.bfirst[ci] + (TERMS && rr >= n ? rr - n : rr);
-            int64_t src = at;
-            if constexpr (PICKS) {
-                const int pick = aux.order[at];
-                src = TERMS ? (rr >= n ? p.P : 0) + pick : pick / p.top_k;  // a chunk's hi rows, then its lo rows
-            } else if (p.gather) {
-                src = p.gather[at];
-                if (src < 0 || src >= p.act_rows) {
-                    if (lane == 0) set_status(p.status, DEV_BAD_COUNT);
-                    src = 0;
-                }
-            }
-            const uint16_t* row = p.x + src * p.K;
-            const uint32_t dst = xbase + r * p.x_stride;
-            for (int c = lane; c < p.K / 8; c += 32) cp16(dst + c * 16, row + c * 8);
-        }
-        cp_commit();
-        int iu = base_u + warp;  // the unit whose stages are being issued: base + warp, + kWarps, ...
-        int ist = 0, islot = 0, ie = 0, iun = 0;
+        // ---- this warp's units (base + warp, + kWarps, ...): the copies run kStages - 1 stages ahead
+        int iu = base_u + warp, ist = 0, islot = 0;
+        const uint8_t *c0 = nullptr, *c1 = nullptr, *zp = nullptr;
+        const uint16_t* sp = nullptr;
+        const uint32_t dst0 = ring + (lane >> 3) * 128;
         auto issue_next = [&]() {
             if (iu < end_u) {
                 if (ist == 0) {
-                    const int v = iu / nu;
-                    ie = aux.be[v];
-                    iun = iu - v * nu;
+                    const int v = iu / nu, un = iu - v * nu;
+                    const int64_t e = aux.be[v];
+                    const int64_t row = e * p.n_out + un * UROWS + (lane >> 3);
+                    c0 = p.q0 + row * (p.K / 2) + (lane & 7) * 16;
+                    c1 = (SWIGLU ? p.q1 + row * (p.K / 2) : p.q0 + (row + 8) * (p.K / 2)) + (lane & 7) * 16;
+                    const int64_t at = (e * p.G + (lane >> 1)) * p.n_out + un * UROWS + (SWIGLU ? 0 : 8 * (lane & 1));
+                    sp = (SWIGLU && (lane & 1) ? p.s1 : p.s0) + at;
+                    if (ZERO) zp = (SWIGLU && (lane & 1) ? p.z1 : p.z0) + at;
                 }
-                issue(ie, iun, ist, islot);
+                const uint32_t base = islot * kStageBytes;
+                if (ist * 8 + (lane & 7) < pieces) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = 4 * j + (lane >> 3);
+                        cp16(dst0 + base + j * 512 + (((lane & 7) ^ ((r * GP) & 7)) << 4),
+                             (j < 2 ? c0 : c1) + (j & 1) * 2 * p.K);
+                    }
+                }
+                if (lane < 2 * NG && ist * NG + (lane >> 1) < p.G) {
+                    cp16(ring + base + kScaleOff + lane * 16, sp);
+                    if (ZERO) cp8(ring + base + kZeroOff + lane * 8, zp);
+                }
+                c0 += kStageCols / 2;
+                c1 += kStageCols / 2;
+                sp += (int64_t)NG * p.n_out;
+                if (ZERO) zp += (int64_t)NG * p.n_out;
                 if (++islot == kStages) islot = 0;
                 if (++ist == nstage) {
                     ist = 0;
@@ -323,139 +304,225 @@ __global__ void __launch_bounds__(kThreads, 1) stream_w4_kernel(const Args p) {
         };
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) issue_next();
-        cp_wait<kStages - 1>();  // the token rows
+
+        // ---- stage the batch's token rows as bytes: a warp per row, a lane per word of 8 columns
+        const int all_rows = aux.brow[nv - 1] + aux.bn[nv - 1];
+        for (int r = warp, ci = 0; r < all_rows; r += kWarps) {
+            while (ci + 1 < nv && aux.brow[ci + 1] <= r) ++ci;
+            const int rr = r - aux.brow[ci];
+            if (rr >= aux.bn[ci]) continue;  // the odd chunk's spare row
+            const int at = aux.off[aux.be[ci]] + aux.bfirst[ci] + rr;
+            int64_t src = at;
+            if constexpr (PICKS) {
+                const int pick = aux.order[at];
+                src = F32X ? pick : pick / p.top_k;
+            } else if (p.gather) {
+                src = p.gather[at];
+                if (src < 0 || src >= p.act_rows) {
+                    if (lane == 0) set_status(p.status, DEV_BAD_COUNT);
+                    src = 0;
+                }
+            }
+            uint8_t* dst = xs + r * p.x_stride;
+            for (int c = lane * 8; c < ((KP + 255) & ~255); c += 256) {
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = 0.f;
+                if (c < p.K) load8<F32X ? DT_F32 : DT_BF16>(p.x, src * p.K + c, v);
+                uint32_t top = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+#pragma unroll
+                for (int o = 2 * GP; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                // c = 2^k: |X| <= 1.984375 * 2^14 (2^22 with three bytes) = 127 * 256, whose signed bytes all fit; k is
+                // one less where the top value is more than 1.984375 times a power of two
+                int k = (TM == 2 ? 14 : 22) - ((int)(top >> 23) - 127) - ((top & 0x7FFFFFu) > 0x7E0000u ? 1 : 0);
+                k = max(-118, min(100, k));
+                const float cs = __uint_as_float((uint32_t)(127 + k) << 23);
+                // a value that is not finite shows in every output of its row
+                const bool finite = top < 0x7F800000u;
+                const float inv = finite ? __uint_as_float((uint32_t)(127 - k) << 23) : __uint_as_float(0x7FC00000u);
+                int X[8], sum = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    X[j] = finite ? __float2int_rn(v[j] * cs) : 0;
+                    sum += X[j];
+                }
+#pragma unroll
+                for (int o = 2 * GP; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (c < KP) {
+                    if ((lane & (4 * GP - 1)) == 0)
+                        meta[(c / GROUP) * meta_rows + r] =
+                            make_float2(inv, TM == 2 ? __int_as_float(sum) : (float)sum);
+#pragma unroll
+                    for (int i = 0; i < TM; ++i) {  // the lowest byte, signed, then what it leaves
+                        uint2 w;                    // columns 0 4 1 5 | 2 6 3 7
+                        w.x = bytes4(X[0], X[4], X[1], X[5]);
+                        w.y = bytes4(X[2], X[6], X[3], X[7]);
+                        *reinterpret_cast<uint2*>(dst + i * KP + c) = w;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) X[j] = (X[j] + 128) >> 8;
+                    }
+                }
+            }
+        }
         __syncthreads();
 
         int slot = 0;
         for (int u = base_u + warp; u < end_u; u += kWarps) {
             const int v = u / nu, un = u - v * nu;
             const int e = aux.be[v], first = aux.bfirst[v], n = aux.bn[v], xrow = aux.brow[v];
-            float acc[NT][4];
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-            // this lane's token row of each column set (rows past the chunk give zeros)
-            uint32_t xa[NT];
-            bool live[NT];
+            // [set][0]: weight row g, [1]: row g + 8; token rows 2 t, 2 t + 1 of the set
+            float2 acc[NT][2];
+            const uint8_t* xa[NT];  // this lane's token row (columns past the chunk repeat its last row)
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                live[i] = TERMS ? g < n : g + 8 * i < n;
-                xa[i] = xbase + (xrow + g + (TERMS ? i * n : 8 * i)) * p.x_stride + t * 16;
+                acc[i][0] = acc[i][1] = make_float2(0.f, 0.f);
+                xa[i] = xs + (xrow + min(8 * i + g, n - 1)) * p.x_stride + t * (8 * GP);
             }
+            const float2* ma = meta + xrow + 2 * t;
             for (int st = 0; st < nstage; ++st) {
                 cp_wait<kStages - 2>();
                 __syncwarp();
-                const uint32_t base = ring + slot * kStageBytes;
-                // sums of one stage, added to the running ones in fp32: the tensor cores' own sums are truncated
-                float part[NT][4];
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) part[i][j] = 0.f;
-                uint32_t s_lo = 0, s_hi = 0, z_lo = 0x43084308u, z_hi = 0x43084308u;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    if (st * 8 + c >= pieces) break;
-                    if ((c & (gp - 1)) == 0) {
-                        const int gr = c / gp;
-                        s_lo = lds16(base + kScaleOff + gr * 32 + 2 * g) * 0x00010001u;
-                        s_hi = lds16(base + kScaleOff + gr * 32 + 16 + 2 * g) * 0x00010001u;
-                        if (ZERO) {
-                            z_lo = 0x43004300u + lds8(base + kZeroOff + gr * 16 + g) * 0x00010001u;
-                            z_hi = 0x43004300u + lds8(base + kZeroOff + gr * 16 + 8 + g) * 0x00010001u;
-                        }
+                const uint8_t* base = smem + (warp * kStages + slot) * kStageBytes;
+                auto do_group = [&](int gi) {
+                    const int gr = st * NG + gi;
+                    uint32_t lo[GP], hi[GP];
+                    const int piece = (gi * GP) ^ ((g * GP) & 7);  // GP pieces share their upper bits with this one
+                    if constexpr (GP == 4) {
+                        const uint4 a = *reinterpret_cast<const uint4*>(base + g * 128 + ((piece ^ t) << 4));
+                        const uint4 b = *reinterpret_cast<const uint4*>(base + (g + 8) * 128 + ((piece ^ t) << 4));
+                        lo[0] = a.x; lo[1] = a.y; lo[2] = a.z; lo[3] = a.w;
+                        hi[0] = b.x; hi[1] = b.y; hi[2] = b.z; hi[3] = b.w;
+                    } else if constexpr (GP == 2) {
+                        const int at = ((piece ^ (t >> 1)) << 4) + (t & 1) * 8;
+                        const uint2 a = *reinterpret_cast<const uint2*>(base + g * 128 + at);
+                        const uint2 b = *reinterpret_cast<const uint2*>(base + (g + 8) * 128 + at);
+                        lo[0] = a.x; lo[1] = a.y;
+                        hi[0] = b.x; hi[1] = b.y;
+                    } else {
+                        lo[0] = *reinterpret_cast<const uint32_t*>(base + g * 128 + (piece << 4) + t * 4);
+                        hi[0] = *reinterpret_cast<const uint32_t*>(base + (g + 8) * 128 + (piece << 4) + t * 4);
                     }
-                    const uint32_t wa = base + g * 128 + ((c ^ g) << 4) + t * 4;
-                    uint32_t a[4], b[4];
-                    unpack(lds32(wa), z_lo, s_lo, a);
-                    unpack(lds32(wa + 8 * 128), z_hi, s_hi, b);
+                    int part[NT][TM][4];
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int k = 0; k < TM; ++k)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) part[i][k][j] = 0;
+                    constexpr int WI = GP == 1 ? 1 : 2;  // words of a token-row read
+#pragma unroll
+                    for (int w = 0; w < GP; w += WI) {
+                        uint32_t a[WI][4];
+#pragma unroll
+                        for (int j = 0; j < WI; ++j) {
+                            a[j][0] = lo[w + j] & 0x0F0F0F0Fu;
+                            a[j][1] = hi[w + j] & 0x0F0F0F0Fu;
+                            a[j][2] = (lo[w + j] >> 4) & 0x0F0F0F0Fu;
+                            a[j][3] = (hi[w + j] >> 4) & 0x0F0F0F0Fu;
+                        }
+#pragma unroll
+                        for (int k = 0; k < TM; ++k)
+#pragma unroll
+                            for (int i = 0; i < NT; ++i) {
+                                const uint8_t* xp = xa[i] + k * KP + gr * GROUP + w * 8;
+                                int(&c)[4] = part[i][k];
+                                if constexpr (WI == 2) {
+                                    const uint4 x = *reinterpret_cast<const uint4*>(xp);
+                                    mma(c, a[0][0], a[0][1], a[0][2], a[0][3], x.x, x.y);
+                                    mma(c, a[WI - 1][0], a[WI - 1][1], a[WI - 1][2], a[WI - 1][3], x.z, x.w);
+                                } else {
+                                    const uint2 x = *reinterpret_cast<const uint2*>(xp);
+                                    mma(c, a[0][0], a[0][1], a[0][2], a[0][3], x.x, x.y);
+                                }
+                            }
+                    }
+                    // ---- y += s / c * (P - z sum X)
+                    const uint16_t* ss = reinterpret_cast<const uint16_t*>(base + kScaleOff + gi * 32);
+                    const float s_lo = bf16_bits_to_f32(ss[g]), s_hi = bf16_bits_to_f32(ss[8 + g]);
+                    const int z_lo = ZERO ? base[kZeroOff + gi * 16 + g] : 8;
+                    const int z_hi = ZERO ? base[kZeroOff + gi * 16 + 8 + g] : 8;
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
-                        uint32_t x[4] = {0u, 0u, 0u, 0u};
-                        if (live[i]) lds128(xa[i] + (st * 8 + c) * 64, x);
-                        mma(part[i], a[0], b[0], a[1], b[1], x[0], x[1]);
-                        mma(part[i], a[2], b[2], a[3], b[3], x[2], x[3]);
+                        const float4 m = *reinterpret_cast<const float4*>(ma + gr * meta_rows + 8 * i);
+                        const float2 inv = make_float2(m.x, m.z);
+                        float d[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float sum = j & 1 ? m.w : m.y;
+                            const int z = j < 2 ? z_lo : z_hi;
+                            const int low = part[i][1][j] * 256 + part[i][0][j];  // below 2^26
+                            if constexpr (TM == 2) d[j] = (float)(low - z * __float_as_int(sum));
+                            else d[j] = fmaf((float)part[i][TM - 1][j], 65536.f, fmaf((float)z, -sum, (float)low));
+                        }
+                        acc[i][0] = fma2(mul2(make_float2(d[0], d[1]), inv), make_float2(s_lo, s_lo), acc[i][0]);
+                        acc[i][1] = fma2(mul2(make_float2(d[2], d[3]), inv), make_float2(s_hi, s_hi), acc[i][1]);
                     }
+                };
+                if ((st + 1) * NG <= p.G) {
+#pragma unroll
+                    for (int gi = 0; gi < NG; ++gi) do_group(gi);
+                } else {
+#pragma unroll 1
+                    for (int gi = 0; gi < p.G - st * NG; ++gi) do_group(gi);
                 }
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] += part[i][j];
                 __syncwarp();  // every lane has read the slot that the next copies overwrite
                 if (++slot == kStages) slot = 0;
                 issue_next();
             }
-            // ---- outputs: rows g (and g + 8) of the unit for token rows 2 t, 2 t + 1 of each set
-            if constexpr (SWIGLU) {
-                uint16_t* h = static_cast<uint16_t*>(p.out);
-                const int f = un * 8 + g;
+            // ---- outputs: weight rows g (and g + 8) of the unit for token rows 2 t, 2 t + 1 of each set
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int r = 8 * i + 2 * t + j;
-                        if (r >= n) continue;
-                        const float gv = acc[i][j], uv = acc[i][2 + j];
-                        const float hv = gv / (1.0f + expf(-gv)) * uv;
-                        const uint32_t hb = f32_to_bf16_bits(hv);
+                for (int j = 0; j < 2; ++j) {
+                    const int r = 8 * i + 2 * t + j;
+                    if (r >= n) continue;
+                    const float lo = j ? acc[i][0].y : acc[i][0].x, hi = j ? acc[i][1].y : acc[i][1].x;
+                    int64_t row = aux.off[e] + first + r;
+                    if constexpr (PICKS) row = aux.order[row];
+                    if constexpr (SWIGLU) {
+                        const float h = lo / (1.0f + expf(-lo)) * hi;
+                        const int64_t at = row * p.n_out + un * 8 + g;
+                        if constexpr (PICKS) static_cast<float*>(p.out)[at] = h;
+                        else static_cast<uint16_t*>(p.out)[at] = (uint16_t)f32_to_bf16_bits(h);
+                    } else {
+                        const int64_t at = row * p.n_out + un * 16 + g;
                         if constexpr (PICKS) {
-                            const int64_t pick = aux.order[aux.off[e] + first + r];
-                            h[pick * p.n_out + f] = (uint16_t)hb;
-                            h[(pick + p.P) * p.n_out + f] = (uint16_t)f32_to_bf16_bits(hv - bf16_bits_to_f32(hb));
+                            static_cast<float*>(p.out)[at] = lo;
+                            static_cast<float*>(p.out)[at + 8] = hi;
                         } else {
-                            h[(int64_t)(aux.off[e] + first + r) * p.n_out + f] = (uint16_t)hb;
+                            static_cast<uint16_t*>(p.out)[at] = (uint16_t)f32_to_bf16_bits(lo);
+                            static_cast<uint16_t*>(p.out)[at + 8] = (uint16_t)f32_to_bf16_bits(hi);
                         }
                     }
-            } else {
-                const int o = un * 16 + g;
-                if constexpr (TERMS) {
-                    float* y = static_cast<float*>(p.out);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int r = 2 * t + j;
-                        if (r >= n) continue;
-                        const int64_t pick = aux.order[aux.off[e] + first + r];
-                        y[pick * p.n_out + o] = acc[0][j] + acc[NT - 1][j];
-                        y[pick * p.n_out + o + 8] = acc[0][2 + j] + acc[NT - 1][2 + j];
-                    }
-                } else {
-                    uint16_t* y = static_cast<uint16_t*>(p.out);
-#pragma unroll
-                    for (int i = 0; i < NT; ++i)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int r = 8 * i + 2 * t + j;
-                            if (r >= n) continue;
-                            uint16_t* row = y + (int64_t)(aux.off[e] + first + r) * p.n_out + o;
-                            row[0] = (uint16_t)f32_to_bf16_bits(acc[i][j]);
-                            row[8] = (uint16_t)f32_to_bf16_bits(acc[i][2 + j]);
-                        }
                 }
-            }
         }
-        cp_wait<0>();  // (empty groups only: the ring is drained)
         b0 = (int64_t)v0 * nu + end_u;
     }
+    cp_wait<0>();  // (empty groups only: every ring is drained)
 }
 
 // token rows per pass and their place in shared memory; false where K is too long for one row
-static bool plan_rows(int K, int NT, bool terms, Args& a, size_t& smem) {
-    const size_t fixed = kRingBytes + ((sizeof(Aux) + 127) & ~size_t(127));
-    a.x_stride = ((K * 2 + 127) & ~127) + 64;  // rows half a 128-byte line apart: the B reads touch every bank once
-    a.xcap = (int)((kSmemLimit - fixed) / a.x_stride);
-    const int per = terms ? 2 : 1;
-    a.chunk_rows = terms ? 8 : 8 * NT;
-    if (a.chunk_rows * per > a.xcap) a.chunk_rows = a.xcap / per;
-    smem = fixed + (size_t)a.xcap * a.x_stride;
-    return a.chunk_rows >= 1;
+static bool plan_rows(int nt, int bytes, int gp, Args& a, size_t& smem) {
+    const int KP = a.G * 32 * gp;
+    // a row's distance modulo 128 bytes: 8 rows' reads (16 bytes of every 32, 16, or 8) then meet no bank twice
+    const int want = gp == 4 ? 16 : (gp == 2 ? 64 : 32);
+    a.x_stride = ((bytes * KP - want + 127) / 128) * 128 + want;
+    const int per_row = a.x_stride + a.G * (int)sizeof(float2);
+    const int fixed = kRingBytes + kAuxBytes + (8 * nt + 1) * a.G * (int)sizeof(float2);
+    a.xcap = (kSmemLimit - fixed) / per_row;
+    if (a.xcap < 1) return false;
+    a.chunk_rows = 8 * nt < a.xcap ? 8 * nt : a.xcap;
+    smem = fixed + (size_t)a.xcap * per_row;
+    return true;
 }
 
-template <bool SWIGLU, bool PICKS, int NT, bool ZERO>
+template <bool SWIGLU, bool PICKS, int NT, int TM, int GP, bool ZERO>
 static cudaError_t run(const Ctx& c, Args a) {
     size_t smem = 0;
-    if (!plan_rows(a.K, NT, PICKS && !SWIGLU, a, smem)) return cudaErrorInvalidValue;
-    auto kern = stream_w4_kernel<SWIGLU, PICKS, NT, ZERO>;
+    if (!plan_rows(NT, TM, GP, a, smem)) return cudaErrorInvalidValue;
+    auto kern = stream_w4_kernel<SWIGLU, PICKS, NT, TM, GP, ZERO>;
     static bool attr_done[64] = {};
     if (c.device < 0 || c.device >= 64) return cudaErrorInvalidDevice;
     if (!attr_done[c.device]) {
@@ -466,9 +533,13 @@ static cudaError_t run(const Ctx& c, Args a) {
     return launch(kern, dim3(c.num_sms), dim3(kThreads), smem, c, a);
 }
 
-template <bool SWIGLU, bool PICKS, int NT>
-static cudaError_t run_z(const Ctx& c, const Args& a) {
-    return a.z0 ? run<SWIGLU, PICKS, NT, true>(c, a) : run<SWIGLU, PICKS, NT, false>(c, a);
+template <bool SWIGLU, bool PICKS, int NT, int TM>
+static cudaError_t run_group(const Ctx& c, const Args& a, int group) {
+    if (group == 32)
+        return a.z0 ? run<SWIGLU, PICKS, NT, TM, 1, true>(c, a) : run<SWIGLU, PICKS, NT, TM, 1, false>(c, a);
+    if (group == 64)
+        return a.z0 ? run<SWIGLU, PICKS, NT, TM, 2, true>(c, a) : run<SWIGLU, PICKS, NT, TM, 2, false>(c, a);
+    return a.z0 ? run<SWIGLU, PICKS, NT, TM, 4, true>(c, a) : run<SWIGLU, PICKS, NT, TM, 4, false>(c, a);
 }
 
 static Args base_args(const W4& w0, const W4& w1, int group, int E, int K, int n_out) {
@@ -478,7 +549,6 @@ static Args base_args(const W4& w0, const W4& w1, int group, int E, int K, int n
     a.E = E;
     a.K = K;
     a.n_out = n_out;
-    a.group = group;
     a.G = (K + group - 1) / group;
     return a;
 }
@@ -486,30 +556,30 @@ static Args base_args(const W4& w0, const W4& w1, int group, int E, int K, int n
 }  // namespace w4s
 
 cudaError_t launch_gate_up_w4_picks(const Ctx& c, const void* v, const W4& Wg, const W4& Wu, int group,
-                                    const int32_t* idx, int T, int k, int E, int d, int d_ff, void* h, int32_t* slot,
-                                    int32_t* status) {
+                                    const int32_t* idx, int T, int k, int E, int d, int d_ff, float* h, int32_t* slot,
+                                    bool exact, int32_t* status) {
     w4s::Args a = w4s::base_args(Wg, Wu, group, E, d, d_ff);
-    a.x = static_cast<const uint16_t*>(v);
+    a.x = v;
     a.picks = idx;
     a.P = T * k;
     a.top_k = k;
     a.out = h;
     a.slot_out = slot;
     a.status = status;
-    // an expert has at most T rows unless a token names it twice: one set of columns covers up to 8
-    return T <= 8 ? w4s::run_z<true, true, 1>(c, a) : w4s::run_z<true, true, 2>(c, a);
+    // few tokens leave an expert a row or two: one set of 8 columns, more passes where they do not
+    return exact ? w4s::run_group<true, true, 1, 3>(c, a, group) : w4s::run_group<true, true, 1, 2>(c, a, group);
 }
 
-cudaError_t launch_down_w4_picks(const Ctx& c, const void* h, const W4& Wd, int group, const int32_t* idx, int T, int k,
-                                 int E, int d, int d_ff, float* y, int32_t* status) {
+cudaError_t launch_down_w4_picks(const Ctx& c, const float* h, const W4& Wd, int group, const int32_t* idx, int T, int k,
+                                 int E, int d, int d_ff, float* y, bool exact, int32_t* status) {
     w4s::Args a = w4s::base_args(Wd, Wd, group, E, d_ff, d);
-    a.x = static_cast<const uint16_t*>(h);
+    a.x = h;
     a.picks = idx;
     a.P = T * k;
     a.top_k = k;
     a.out = y;
     a.status = status;
-    return w4s::run_z<false, true, 2>(c, a);
+    return exact ? w4s::run_group<false, true, 1, 3>(c, a, group) : w4s::run_group<false, true, 1, 2>(c, a, group);
 }
 
 cudaError_t launch_gate_up_w4(const Ctx& c, const void* xp, const W4& Wg, const W4& Wu, int group, const int32_t* counts,
@@ -517,7 +587,7 @@ cudaError_t launch_gate_up_w4(const Ctx& c, const void* xp, const W4& Wg, const 
                               const int32_t* gather, int act_rows) {
     if (S == 0) return cudaSuccess;
     w4s::Args a = w4s::base_args(Wg, Wu, group, E, d, d_ff);
-    a.x = static_cast<const uint16_t*>(xp);
+    a.x = xp;
     a.gather = gather;
     a.act_rows = act_rows;
     a.counts = counts;
@@ -525,20 +595,22 @@ cudaError_t launch_gate_up_w4(const Ctx& c, const void* xp, const W4& Wg, const 
     a.P = S;
     a.out = h;
     a.status = status;
-    return S <= 2 * E ? w4s::run_z<true, false, 1>(c, a) : w4s::run_z<true, false, 2>(c, a);
+    return S <= 2 * E ? w4s::run_group<true, false, 1, 2>(c, a, group)
+                      : w4s::run_group<true, false, 2, 2>(c, a, group);
 }
 
 cudaError_t launch_down_w4(const Ctx& c, const void* h, const W4& Wd, int group, const int32_t* counts,
                            const int32_t* offsets, int S, int E, int d, int d_ff, void* y, int32_t* status) {
     if (S == 0) return cudaSuccess;
     w4s::Args a = w4s::base_args(Wd, Wd, group, E, d_ff, d);
-    a.x = static_cast<const uint16_t*>(h);
+    a.x = h;
     a.counts = counts;
     a.offsets = offsets;
     a.P = S;
     a.out = y;
     a.status = status;
-    return S <= 2 * E ? w4s::run_z<false, false, 1>(c, a) : w4s::run_z<false, false, 2>(c, a);
+    return S <= 2 * E ? w4s::run_group<false, false, 1, 2>(c, a, group)
+                      : w4s::run_group<false, false, 2, 2>(c, a, group);
 }
 
 }  // namespace moe

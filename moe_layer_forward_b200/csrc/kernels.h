@@ -156,13 +156,13 @@ cudaError_t launch_quant_w4(const Ctx& c, const void* x, int dt, int E, int64_t 
                             uint16_t* s, uint8_t* z);
 cudaError_t launch_dequant_w4(const Ctx& c, const uint8_t* q, const uint16_t* s, const uint8_t* z, int E, int64_t n, int k,
                               int group, void* out, int dt);
-// from the router's picks (T k <= 256): h keeps two bf16 terms [2][T k][d_ff], y [T k][d] is fp32; slot gets the
-// identity map for the combine (-1 for a bad id)
+// from the router's picks (T k <= 256): h [T k][d_ff] and y [T k][d] are fp32; slot gets the identity map for the
+// combine (-1 for a bad id); exact: the rows enter the products with 24 bits (else 16)
 cudaError_t launch_gate_up_w4_picks(const Ctx& c, const void* v, const W4& Wg, const W4& Wu, int group,
-                                    const int32_t* idx, int T, int k, int E, int d, int d_ff, void* h, int32_t* slot,
-                                    int32_t* status);
-cudaError_t launch_down_w4_picks(const Ctx& c, const void* h, const W4& Wd, int group, const int32_t* idx, int T, int k,
-                                 int E, int d, int d_ff, float* y, int32_t* status);
+                                    const int32_t* idx, int T, int k, int E, int d, int d_ff, float* h, int32_t* slot,
+                                    bool exact, int32_t* status);
+cudaError_t launch_down_w4_picks(const Ctx& c, const float* h, const W4& Wd, int group, const int32_t* idx, int T, int k,
+                                 int E, int d, int d_ff, float* y, bool exact, int32_t* status);
 // moe_forward_w4 takes that form: few tokens, so that experts have a row or two each
 inline bool w4_use_picks(int T, int k, int E) { return T * k <= 128 && (T <= 8 || T * k <= 2 * E); }
 // expert-contiguous rows; gather (gate/up): slot i reads row gather[i] of act_rows rows

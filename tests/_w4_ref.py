@@ -65,10 +65,34 @@ def acc_bound(x, w, k):
     return (k / 16 + 16) * 2.0 ** -23 * (x.abs() @ w.abs().T)
 
 
-def gate_up(x, wg, wu):
+def row_bound(x, w, group, bits):
+    """The share of rows that enter the products rounded to 2^-bits of the largest value of their group."""
+    k = x.shape[1]
+    G = -(-k // group)
+    padded = torch.zeros((x.shape[0], G * group), dtype=x.dtype)
+    padded[:, :k] = x.abs()
+    top = padded.reshape(-1, G, group).amax(-1)
+    return 2.0 ** -bits * (top.repeat_interleave(group, 1)[:, :k] @ w.abs().T)
+
+
+def product_bound(x, w, group, bits=15):
+    return acc_bound(x, w, x.shape[1]) + row_bound(x, w, group, bits)
+
+
+def gate_up(x, wg, wu, group, bits=15):
     """fp64 h and its bound before h is rounded: silu' is below 1.1, |silu(a) - silu(b)| <= 1.1 |a - b|."""
     g, u = x @ wg.T, x @ wu.T
-    k = x.shape[1]
-    dg, du = acc_bound(x, wg, k), acc_bound(x, wu, k)
+    dg, du = product_bound(x, wg, group, bits), product_bound(x, wu, group, bits)
     h = silu(g) * u
     return h, 1.1 * dg * u.abs() + silu(g).abs() * du + 1.1 * dg * du + 2.0 ** -20 * h.abs()
+
+
+def readings(*weights):
+    """The matrices' fp64 weights in the two readings that a call may take: exact, and rounded to bf16."""
+    for rounded in (False, True):
+        yield [dequant(*w, rounded=rounded) for w in weights]
+
+
+def within(got, want, tol, half):
+    """got is want up to tol before it was rounded by at most half of its value."""
+    return bool(((got - want).abs() <= tol + half * (want.abs() + tol) + 1e-30).all())
