@@ -781,7 +781,8 @@ moe_status_t moe_forward_w4(const moe_shape_t* shape, const moe_weights_w4_t* w,
     float* wgt = topk_w ? topk_w : wgt_ws;
     PicksWs pw{};
     int32_t *hist = nullptr, *counts = nullptr, *offsets = nullptr, *slot_token = nullptr, *token_slot = nullptr;
-    void *h = nullptr, *y = nullptr;
+    void *xp = nullptr, *h = nullptr, *y = nullptr;
+    const bool in_place = w4_few_rows(S, E);  // the weight stream reads the rows through slot_token
     if (picks) {
         pw = carve_picks(cv, S, d, d_ff);
     } else {
@@ -790,6 +791,7 @@ moe_status_t moe_forward_w4(const moe_shape_t* shape, const moe_weights_w4_t* w,
         offsets = static_cast<int32_t*>(cv.take((size_t)(E + 1) * sizeof(int32_t)));
         slot_token = static_cast<int32_t*>(cv.take((size_t)S * sizeof(int32_t)));
         token_slot = static_cast<int32_t*>(cv.take((size_t)S * sizeof(int32_t)));
+        if (!in_place) xp = cv.take((size_t)S * d * 2);
         h = cv.take((size_t)S * d_ff * 2);
         y = cv.take((size_t)S * d * 2);
     }
@@ -818,13 +820,13 @@ moe_status_t moe_forward_w4(const moe_shape_t* shape, const moe_weights_w4_t* w,
     if (st != MOE_OK) return st;
     if (picks)
         return run_picks(c, v, w, idx, wgt, x, shape->x_dtype, T, k, E, d, d_ff, out, shape->out_dtype, pw, dev_status);
-    // 3. permutation maps only: gate/up reads the rows in place
-    st = cuda_status(launch_permute(c, nullptr, MOE_BF16, idx, T, d, E, k, counts, offsets, slot_token, token_slot,
-                                    nullptr, hist, dev_status));
+    // 3. permutation, with the row copy where the expert kernel wants contiguous rows
+    st = cuda_status(
+        launch_permute(c, v, MOE_BF16, idx, T, d, E, k, counts, offsets, slot_token, token_slot, xp, hist, dev_status));
     if (st != MOE_OK) return st;
     // 4. 4-bit SwiGLU MLP
-    st = cuda_status(launch_gate_up_w4(c, v, to_w4(w->W_gate), to_w4(w->W_up), w->group, counts, offsets, S, E, d, d_ff, h,
-                                       dev_status, slot_token, T));
+    st = cuda_status(launch_gate_up_w4(c, in_place ? v : xp, to_w4(w->W_gate), to_w4(w->W_up), w->group, counts, offsets,
+                                       S, E, d, d_ff, h, dev_status, in_place ? slot_token : nullptr, T));
     if (st != MOE_OK) return st;
     st = cuda_status(launch_down_w4(c, h, to_w4(w->W_down), w->group, counts, offsets, S, E, d, d_ff, y, dev_status));
     if (st != MOE_OK) return st;

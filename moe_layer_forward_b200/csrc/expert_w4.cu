@@ -39,9 +39,13 @@
 namespace moe {
 namespace w4s {
 
-constexpr int kWarps = 12;
+#ifndef W4W
+#define W4W 12
+#define W4S 3
+#endif
+constexpr int kWarps = W4W;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 3;
+constexpr int kStages = W4S;
 constexpr int kStageCols = 256;
 constexpr int kCodeBytes = 16 * (kStageCols / 2);            // 16 rows x 128 bytes
 constexpr int kScaleOff = kCodeBytes;                        // [group][16 rows] bf16
@@ -50,6 +54,7 @@ constexpr int kStageBytes = kZeroOff + (kStageCols / 32) * 16;
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kSmemLimit = 232448;
 constexpr int kMaxPicks = 256;
+constexpr int kMaxRows = 32 * 16;  // staged rows: 32 chunks of at most 16
 static_assert(kThreads >= kMaxPicks, "a thread per pick");
 
 struct Args {
@@ -85,6 +90,7 @@ struct Aux {
     // the current batch's chunks: expert, first row, rows, first staged row
     int b_n;
     int be[32], bfirst[32], bn[32], brow[32];
+    int src[kMaxRows];  // input row of a staged row
 };
 constexpr int kAuxBytes = (sizeof(Aux) + 127) & ~127;
 
@@ -120,6 +126,24 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     return *reinterpret_cast<float2*>(&r);
 }
 
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+    return *reinterpret_cast<float2*>(&r);
+}
+
+template <int V>
+struct Int {
+    static constexpr int value = V;
+};
+template <bool V>
+struct Bool {
+    static constexpr bool value = V;
+};
+
+constexpr int kMagic = 0x4B400000;  // the bits of 1.5 * 2^23: plus an integer below 2^22 they are that number's sum
+__host__ __device__ constexpr int meta_rows(int xcap, int nt) { return (xcap + 8 * nt + 1) & ~1; }
+
 // four signed bytes, lowest first, of the low bytes of four integers
 __device__ __forceinline__ uint32_t bytes4(int a, int b, int c, int d) {
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
@@ -134,10 +158,12 @@ __global__ void __launch_bounds__(kThreads, 1) stream_w4_kernel(const Args p) {
     constexpr int NG = kStageCols / GROUP;  // groups of a stage
     extern __shared__ __align__(128) uint8_t smem[];
     Aux& aux = *reinterpret_cast<Aux*>(smem + kRingBytes);
-    // per (group, row): 1 / c, and the sum of X (an integer with two bytes, fp32 with three)
-    float2* meta = reinterpret_cast<float2*>(smem + kRingBytes + kAuxBytes);
-    const int meta_rows = (p.xcap + 8 * NT + 1) & ~1;
-    uint8_t* xs = smem + kRingBytes + kAuxBytes + p.G * meta_rows * (int)sizeof(float2);
+    // [G][rows] 1 / c, then per byte [G][rows] where the group's integer sum starts (without zero points: kMagic - 8
+    // times the sum of the byte; with them: the sum)
+    const int mrows = meta_rows(p.xcap, NT);
+    float* meta = reinterpret_cast<float*>(smem + kRingBytes + kAuxBytes);
+    const int mplane = p.G * mrows;
+    uint8_t* xs = smem + kRingBytes + kAuxBytes + (((1 + TM) * mplane * 4 + 15) & ~15);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int E = p.E;
 
@@ -305,30 +331,52 @@ __global__ void __launch_bounds__(kThreads, 1) stream_w4_kernel(const Args p) {
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) issue_next();
 
-        // ---- stage the batch's token rows as bytes: a warp per row, a lane per word of 8 columns
+        // ---- stage the batch's token rows as bytes: a warp per (row, 256 columns), a lane per word of 8 columns;
+        // the loads of several such pieces are in flight together
         const int all_rows = aux.brow[nv - 1] + aux.bn[nv - 1];
-        for (int r = warp, ci = 0; r < all_rows; r += kWarps) {
+        for (int r = tid; r < all_rows; r += kThreads) {
+            int ci = 0;
             while (ci + 1 < nv && aux.brow[ci + 1] <= r) ++ci;
             const int rr = r - aux.brow[ci];
-            if (rr >= aux.bn[ci]) continue;  // the odd chunk's spare row
-            const int at = aux.off[aux.be[ci]] + aux.bfirst[ci] + rr;
-            int64_t src = at;
-            if constexpr (PICKS) {
-                const int pick = aux.order[at];
-                src = F32X ? pick : pick / p.top_k;
-            } else if (p.gather) {
-                src = p.gather[at];
-                if (src < 0 || src >= p.act_rows) {
-                    if (lane == 0) set_status(p.status, DEV_BAD_COUNT);
-                    src = 0;
+            int src = -1;  // the spare row after an odd chunk
+            if (rr < aux.bn[ci]) {
+                src = aux.off[aux.be[ci]] + aux.bfirst[ci] + rr;
+                if constexpr (PICKS) {
+                    const int pick = aux.order[src];
+                    src = F32X ? pick : pick / p.top_k;
+                } else if (p.gather) {
+                    src = p.gather[src];
+                    if (src < 0 || src >= p.act_rows) {
+                        set_status(p.status, DEV_BAD_COUNT);
+                        src = 0;
+                    }
                 }
             }
-            uint8_t* dst = xs + r * p.x_stride;
-            for (int c = lane * 8; c < ((KP + 255) & ~255); c += 256) {
-                float v[8];
+            aux.src[r] = src;
+        }
+        __syncthreads();
+        const int blocks = (KP + 255) >> 8, items = all_rows * blocks;
+        constexpr int kAhead = F32X ? 2 : 4;
+        for (int it0 = warp; it0 < items; it0 += kAhead * kWarps) {
+            float vv[kAhead][8];
+            int rows[kAhead], cols[kAhead];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = 0.f;
-                if (c < p.K) load8<F32X ? DT_F32 : DT_BF16>(p.x, src * p.K + c, v);
+            for (int q = 0; q < kAhead; ++q) {
+                const int it = it0 + q * kWarps;
+                rows[q] = it / blocks;
+                cols[q] = (it - rows[q] * blocks) * 256 + lane * 8;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) vv[q][j] = 0.f;
+                const int src = it < items ? aux.src[rows[q]] : -1;
+                if (src < 0) rows[q] = -1;
+                else if (cols[q] < p.K) load8<F32X ? DT_F32 : DT_BF16>(p.x, (int64_t)src * p.K + cols[q], vv[q]);
+            }
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                const int r = rows[q], c = cols[q];
+                if (r < 0) continue;
+                float(&v)[8] = vv[q];
+                uint8_t* dst = xs + r * p.x_stride;
                 uint32_t top = 0;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
@@ -342,45 +390,50 @@ __global__ void __launch_bounds__(kThreads, 1) stream_w4_kernel(const Args p) {
                 // a value that is not finite shows in every output of its row
                 const bool finite = top < 0x7F800000u;
                 const float inv = finite ? __uint_as_float((uint32_t)(127 - k) << 23) : __uint_as_float(0x7FC00000u);
-                int X[8], sum = 0;
+                int X[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    X[j] = finite ? __float2int_rn(v[j] * cs) : 0;
-                    sum += X[j];
-                }
+                for (int j = 0; j < 8; ++j) X[j] = finite ? __float2int_rn(v[j] * cs) : 0;
+                const bool in = c < KP, first = in && (lane & (4 * GP - 1)) == 0;
+                float* m = meta + (c / GROUP) * mrows + r;
+                if (first) m[0] = inv;
 #pragma unroll
-                for (int o = 2 * GP; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (c < KP) {
-                    if ((lane & (4 * GP - 1)) == 0)
-                        meta[(c / GROUP) * meta_rows + r] =
-                            make_float2(inv, TM == 2 ? __int_as_float(sum) : (float)sum);
+                for (int i = 0; i < TM; ++i) {  // the lowest byte, signed, then what it leaves
+                    uint2 w;                    // columns 0 4 1 5 | 2 6 3 7
+                    w.x = bytes4(X[0], X[4], X[1], X[5]);
+                    w.y = bytes4(X[2], X[6], X[3], X[7]);
+                    if (in) *reinterpret_cast<uint2*>(dst + i * KP + c) = w;
+                    int sum = __dp4a((int)w.x, 0x01010101, __dp4a((int)w.y, 0x01010101, 0));
 #pragma unroll
-                    for (int i = 0; i < TM; ++i) {  // the lowest byte, signed, then what it leaves
-                        uint2 w;                    // columns 0 4 1 5 | 2 6 3 7
-                        w.x = bytes4(X[0], X[4], X[1], X[5]);
-                        w.y = bytes4(X[2], X[6], X[3], X[7]);
-                        *reinterpret_cast<uint2*>(dst + i * KP + c) = w;
+                    for (int o = 2 * GP; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (first) m[(1 + i) * mplane] = __int_as_float(ZERO ? sum : kMagic - 8 * sum);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) X[j] = (X[j] + 128) >> 8;
-                    }
+                    for (int j = 0; j < 8; ++j) X[j] = (X[j] + 128) >> 8;
                 }
             }
         }
         __syncthreads();
 
         int slot = 0;
-        for (int u = base_u + warp; u < end_u; u += kWarps) {
+        // one unit with its n token rows in SETS sets of columns.  PACKED: one set holds all bytes of up to PR rows
+        // (column = byte * PR + row); else set i is rows 8 i .. 8 i + 7 and every byte is a product of its own.
+        auto unit = [&](auto sets_c, auto packed_c, int u) {
+            constexpr int SETS = decltype(sets_c)::value;
+            constexpr bool PACKED = decltype(packed_c)::value;
+            constexpr int PR = 8 / TM;                // rows of a packed set
+            constexpr int BYTES = PACKED ? 1 : TM;    // products per set
             const int v = u / nu, un = u - v * nu;
             const int e = aux.be[v], first = aux.bfirst[v], n = aux.bn[v], xrow = aux.brow[v];
-            // [set][0]: weight row g, [1]: row g + 8; token rows 2 t, 2 t + 1 of the set
-            float2 acc[NT][2];
-            const uint8_t* xa[NT];  // this lane's token row (columns past the chunk repeat its last row)
+            // [set][0]: weight row g, [1]: row g + 8; the pair: columns 2 t, 2 t + 1 of the set
+            float2 acc[SETS][2];
+            const uint8_t* xa[SETS];  // this lane's column (rows past the chunk repeat its last one)
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
+            for (int i = 0; i < SETS; ++i) {
                 acc[i][0] = acc[i][1] = make_float2(0.f, 0.f);
-                xa[i] = xs + (xrow + min(8 * i + g, n - 1)) * p.x_stride + t * (8 * GP);
+                const int row = PACKED ? g % PR : 8 * i + g;
+                xa[i] = xs + (xrow + min(row, n - 1)) * p.x_stride + t * (8 * GP) + (PACKED ? min(g / PR, TM - 1) * KP : 0);
             }
-            const float2* ma = meta + xrow + 2 * t;
+            const float* ma = meta + xrow + (PACKED ? (2 * t) % PR : 2 * t);
+            const float* mc = ma + (1 + (PACKED ? min(2 * t / PR, TM - 1) : 0)) * mplane;
             for (int st = 0; st < nstage; ++st) {
                 cp_wait<kStages - 2>();
                 __syncwarp();
@@ -404,13 +457,24 @@ __global__ void __launch_bounds__(kThreads, 1) stream_w4_kernel(const Args p) {
                         lo[0] = *reinterpret_cast<const uint32_t*>(base + g * 128 + (piece << 4) + t * 4);
                         hi[0] = *reinterpret_cast<const uint32_t*>(base + (g + 8) * 128 + (piece << 4) + t * 4);
                     }
-                    int part[NT][TM][4];
+                    // the integer sums start at kMagic - z * (sum of the bytes): read as floats they are then
+                    // 1.5 * 2^23 plus the group's sum, with no conversion
+                    int part[SETS][BYTES][4];
+                    int z_lo = 0, z_hi = 0;
+                    if (ZERO) {
+                        z_lo = base[kZeroOff + gi * 16 + g];
+                        z_hi = base[kZeroOff + gi * 16 + 8 + g];
+                    }
 #pragma unroll
-                    for (int i = 0; i < NT; ++i)
+                    for (int i = 0; i < SETS; ++i)
 #pragma unroll
-                        for (int k = 0; k < TM; ++k)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) part[i][k][j] = 0;
+                        for (int k = 0; k < BYTES; ++k) {
+                            const int2 m = *reinterpret_cast<const int2*>(mc + k * mplane + gr * mrows + 8 * i);
+                            part[i][k][0] = ZERO ? kMagic - z_lo * m.x : m.x;
+                            part[i][k][1] = ZERO ? kMagic - z_lo * m.y : m.y;
+                            part[i][k][2] = ZERO ? kMagic - z_hi * m.x : m.x;
+                            part[i][k][3] = ZERO ? kMagic - z_hi * m.y : m.y;
+                        }
                     constexpr int WI = GP == 1 ? 1 : 2;  // words of a token-row read
 #pragma unroll
                     for (int w = 0; w < GP; w += WI) {
@@ -423,9 +487,9 @@ __global__ void __launch_bounds__(kThreads, 1) stream_w4_kernel(const Args p) {
                             a[j][3] = (hi[w + j] >> 4) & 0x0F0F0F0Fu;
                         }
 #pragma unroll
-                        for (int k = 0; k < TM; ++k)
+                        for (int k = 0; k < BYTES; ++k)
 #pragma unroll
-                            for (int i = 0; i < NT; ++i) {
+                            for (int i = 0; i < SETS; ++i) {
                                 const uint8_t* xp = xa[i] + k * KP + gr * GROUP + w * 8;
                                 int(&c)[4] = part[i][k];
                                 if constexpr (WI == 2) {
@@ -441,23 +505,23 @@ __global__ void __launch_bounds__(kThreads, 1) stream_w4_kernel(const Args p) {
                     // ---- y += s / c * (P - z sum X)
                     const uint16_t* ss = reinterpret_cast<const uint16_t*>(base + kScaleOff + gi * 32);
                     const float s_lo = bf16_bits_to_f32(ss[g]), s_hi = bf16_bits_to_f32(ss[8 + g]);
-                    const int z_lo = ZERO ? base[kZeroOff + gi * 16 + g] : 8;
-                    const int z_hi = ZERO ? base[kZeroOff + gi * 16 + 8 + g] : 8;
+                    const float2 magic = make_float2(-12582912.f, -12582912.f), k256 = make_float2(256.f, 256.f);
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        const float4 m = *reinterpret_cast<const float4*>(ma + gr * meta_rows + 8 * i);
-                        const float2 inv = make_float2(m.x, m.z);
-                        float d[4];
+                    for (int i = 0; i < SETS; ++i) {
+                        const float2 inv = *reinterpret_cast<const float2*>(ma + gr * mrows + 8 * i);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float sum = j & 1 ? m.w : m.y;
-                            const int z = j < 2 ? z_lo : z_hi;
-                            const int low = part[i][1][j] * 256 + part[i][0][j];  // below 2^26
-                            if constexpr (TM == 2) d[j] = (float)(low - z * __float_as_int(sum));
-                            else d[j] = fmaf((float)part[i][TM - 1][j], 65536.f, fmaf((float)z, -sum, (float)low));
+                        for (int h = 0; h < 2; ++h) {
+                            float2 d = make_float2(0.f, 0.f);
+#pragma unroll
+                            for (int k = BYTES - 1; k >= 0; --k) {
+                                const float2 f = add2(
+                                    make_float2(__int_as_float(part[i][k][2 * h]), __int_as_float(part[i][k][2 * h + 1])),
+                                    magic);
+                                d = k == BYTES - 1 ? f : fma2(d, k256, f);
+                            }
+                            const float sc = h ? s_hi : s_lo;
+                            acc[i][h] = fma2(mul2(d, inv), make_float2(sc, sc), acc[i][h]);
                         }
-                        acc[i][0] = fma2(mul2(make_float2(d[0], d[1]), inv), make_float2(s_lo, s_lo), acc[i][0]);
-                        acc[i][1] = fma2(mul2(make_float2(d[2], d[3]), inv), make_float2(s_hi, s_hi), acc[i][1]);
                     }
                 };
                 if ((st + 1) * NG <= p.G) {
@@ -471,13 +535,28 @@ __global__ void __launch_bounds__(kThreads, 1) stream_w4_kernel(const Args p) {
                 if (++slot == kStages) slot = 0;
                 issue_next();
             }
+            if constexpr (PACKED) {  // the bytes of a row are columns of neighbouring lanes
+                const int b = 2 * t / PR;
+                const float k = b == 0 ? 1.f : (b == 1 ? 256.f : (b < TM ? 65536.f : 0.f));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float2& a = acc[0][h];
+                    a.x = b < TM ? a.x * k : 0.f;
+                    a.y = b < TM ? a.y * k : 0.f;
+#pragma unroll
+                    for (int o = PR / 2; o < 4; o <<= 1) {
+                        a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+                        a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
+                    }
+                }
+            }
             // ---- outputs: weight rows g (and g + 8) of the unit for token rows 2 t, 2 t + 1 of each set
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < SETS; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int r = 8 * i + 2 * t + j;
-                    if (r >= n) continue;
+                    if (r >= n) continue;  // (packed: n <= PR, so the lanes of the first byte store)
                     const float lo = j ? acc[i][0].y : acc[i][0].x, hi = j ? acc[i][1].y : acc[i][1].x;
                     int64_t row = aux.off[e] + first + r;
                     if constexpr (PICKS) row = aux.order[row];
@@ -497,6 +576,12 @@ __global__ void __launch_bounds__(kThreads, 1) stream_w4_kernel(const Args p) {
                         }
                     }
                 }
+        };
+        for (int u = base_u + warp; u < end_u; u += kWarps) {
+            const int n = aux.bn[u / nu];
+            if (n <= 8 / TM) unit(Int<1>{}, Bool<true>{}, u);
+            else if (NT == 1 || n <= 8) unit(Int<1>{}, Bool<false>{}, u);
+            else unit(Int<NT>{}, Bool<false>{}, u);
         }
         b0 = (int64_t)v0 * nu + end_u;
     }
@@ -509,12 +594,13 @@ static bool plan_rows(int nt, int bytes, int gp, Args& a, size_t& smem) {
     // a row's distance modulo 128 bytes: 8 rows' reads (16 bytes of every 32, 16, or 8) then meet no bank twice
     const int want = gp == 4 ? 16 : (gp == 2 ? 64 : 32);
     a.x_stride = ((bytes * KP - want + 127) / 128) * 128 + want;
-    const int per_row = a.x_stride + a.G * (int)sizeof(float2);
-    const int fixed = kRingBytes + kAuxBytes + (8 * nt + 1) * a.G * (int)sizeof(float2);
-    a.xcap = (kSmemLimit - fixed) / per_row;
+    const int meta = (1 + bytes) * a.G * 4;  // of a row
+    const int fixed = kRingBytes + kAuxBytes + (8 * nt + 2) * meta + 16;
+    a.xcap = (kSmemLimit - fixed) / (a.x_stride + meta);
     if (a.xcap < 1) return false;
+    if (a.xcap > kMaxRows) a.xcap = kMaxRows;
     a.chunk_rows = 8 * nt < a.xcap ? 8 * nt : a.xcap;
-    smem = fixed + (size_t)a.xcap * per_row;
+    smem = fixed + (size_t)a.xcap * (a.x_stride + meta);
     return true;
 }
 
@@ -586,6 +672,10 @@ cudaError_t launch_gate_up_w4(const Ctx& c, const void* xp, const W4& Wg, const 
                               const int32_t* offsets, int S, int E, int d, int d_ff, void* h, int32_t* status,
                               const int32_t* gather, int act_rows) {
     if (S == 0) return cudaSuccess;
+    if (!w4_few_rows(S, E)) {
+        if (gather) return cudaErrorInvalidValue;
+        return launch_gate_up_w4_tc(c, xp, Wg, Wu, group, counts, offsets, S, E, d, d_ff, h, status);
+    }
     w4s::Args a = w4s::base_args(Wg, Wu, group, E, d, d_ff);
     a.x = xp;
     a.gather = gather;
@@ -602,6 +692,7 @@ cudaError_t launch_gate_up_w4(const Ctx& c, const void* xp, const W4& Wg, const 
 cudaError_t launch_down_w4(const Ctx& c, const void* h, const W4& Wd, int group, const int32_t* counts,
                            const int32_t* offsets, int S, int E, int d, int d_ff, void* y, int32_t* status) {
     if (S == 0) return cudaSuccess;
+    if (!w4_few_rows(S, E)) return launch_down_w4_tc(c, h, Wd, group, counts, offsets, S, E, d, d_ff, y, status);
     w4s::Args a = w4s::base_args(Wd, Wd, group, E, d_ff, d);
     a.x = h;
     a.counts = counts;

@@ -1,0 +1,696 @@
+// 4-bit experts for many rows per expert: grouped products on tcgen05 with the weights unpacked into tensor memory.
+//
+//   gate/up   h = SiLU(x Wg^T) * (x Wu^T)       down   y = h Wd^T       per expert segment, w = bf16((q - z) s)
+//
+// The weights are the MMA's M operand (128 weight rows = TMEM lanes), the expert's token rows its N.  A tile has
+// two such operands (gate and up of 128 features, or 256 features of down) against up to R token rows, so that
+// each staged token slice feeds two MMAs.  Codes arrive by TMA as they are stored; eight warps unpack them, a
+// weight row per thread, and store the bf16 weights straight to tensor memory as the A operand: they never pass
+// through shared memory, whose bandwidth is what paces the bf16 kernels (expert_tc_dual.cu).
+//
+// Unpacking, 9 instructions for 8 weights.  A nibble masked in place is a subnormal (or first-binade) bf16,
+// q 2^-133 in bits 0..3 and q 2^-129 in bits 4..7, so one packed FMA does the rest:
+//   w 2^-16 = q 2^-133 * (s 2^117) - z s 2^-16
+// It rounds once, and the last term is exact for z = 8 or scales of at most 4 significant bits, the quantiser's.
+// Other scales with zero points, and scales of 2^11 or more (s 2^117 would overflow), take 128 + q, a subtraction
+// and a product.  The epilogue multiplies the 2^16 back.
+//
+// What bounds it: the codes' bytes up to about 65 rows per expert, the tensor cores above.
+//
+// Warp roles (1 CTA per SM, 832 threads):
+//   warps 0..15  unpack: warp w the TMEM lane quarter w % 4 of operand (w / 4) % 2, columns 64 (w / 8) .. + 63 of
+//                every stage, into a ring of four A slots (64 columns of both operands).  Sixteen, because a
+//                warp's chain (codes, scale, unpack, store, wait) is long and its work per stage short
+//   warps 16..23 epilogue: warp w the quarter w % 4; gate/up: the even or odd 32-row pieces of the tile, down: one
+//                of the two operands.  A piece is transposed through 2 KB of shared memory of the warp's own.
+//   warp 24      TMA producer: a ring of code stages (128 columns of both operands, scales, zero points) and one of
+//                token stages (R rows x 128 columns)
+//   warp 25      owns the TMEM allocation; lane 0 issues the MMAs and commits
+// Tensor memory: columns 0..255 accumulators (R <= 64: two buffers of gate | up, else one), 256..511 the A ring.
+// Every wait is bounded; a wait that gives up raises DEV_TIMEOUT and all roles unwind as in expert_tc.cu.
+#include <cuda.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace w4t {
+using namespace tc;
+
+constexpr int kThreads = 832;
+constexpr int kProducer = 24, kIssuer = 25;
+constexpr int kSmemLimit = 232448;
+constexpr int kCols = 128;                    // columns of a stage
+constexpr int kOpBytes = 128 * (kCols / 2);   // codes of one operand's stage
+constexpr int kScaleBytes = 4 * 256;          // up to 4 groups x 128 rows
+constexpr int kZeroBytes = 4 * 128;
+constexpr int kStageBytes = 2 * (kOpBytes + kScaleBytes + kZeroBytes);
+constexpr int kStageStride = (kStageBytes + 1023) & ~1023;
+constexpr int kMaxStages = 8;
+constexpr int kSlots = 4;
+constexpr int kEpiBytes = 8 * 2048;
+constexpr int kAuxBytes = 4096;
+
+struct Args {
+    const int32_t* counts;
+    const int32_t* offsets;
+    int E, K, n_out, G;
+    int R;        // token rows per tile: 16, 32, 64 or 128
+    int cstages;  // code stages
+    int xstages;  // token stages
+    uint16_t* out;
+    int32_t* status;
+    int S;  // rows of the expert-contiguous buffers; a segment that does not fit is clamped and flagged
+    // bounded waits: the limit of one wait, and (failure-path tests only) an extra wait on a barrier that
+    // nothing completes, made by the epilogue warps before their first tile
+    uint64_t wait_ns = kTimeoutNs;
+    int stall = 0;
+};
+
+struct Aux {
+    uint64_t cfull[kMaxStages];
+    uint64_t cempty[kMaxStages];
+    uint64_t xfull[kMaxStages];
+    uint64_t xempty[kMaxStages];
+    uint64_t afull[kSlots];
+    uint64_t aempty[kSlots];
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    uint64_t drain;
+    uint64_t never;  // completed by nothing: the injected stall waits on it
+    uint32_t tmem_slot;
+    int abort_flag;
+    int tstart[kMaxExperts + 1];
+    int cnt[kMaxExperts];
+    int off[kMaxExperts];
+};
+static_assert(sizeof(Aux) <= kAuxBytes, "aux block");
+
+__device__ __forceinline__ void decode_tile(const Aux& a, int E, int R, int tile, int& e, int& rb, int& cb) {
+    int lo = 0, hi = E - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.tstart[mid] <= tile) lo = mid; else hi = mid - 1;
+    }
+    e = lo;
+    const int local = tile - a.tstart[e];
+    const int nrb = (a.cnt[e] + R - 1) / R;
+    cb = local / nrb;
+    rb = local - cb * nrb;
+}
+
+// mbar_wait with the timer read late: the roles here hand over every 64 columns, most waits are short but fail their
+// first try, and reading the timer costs more than the rest of the hand-over.
+static __device__ __noinline__ bool wait_late(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 255u) == 0u) {
+            if (*abort_flag) return false;
+            const uint64_t now = globaltimer();
+            if (t0 == 0) t0 = now;
+            else if (now - t0 > limit_ns) return false;
+        }
+    }
+}
+__device__ __forceinline__ bool quick_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
+    const bool ok = mbar_try_wait(bar, parity) || wait_late(bar, parity, abort_flag, limit_ns);
+    return __all_sync(0xffffffffu, ok);
+}
+
+// One lane of a converged warp, the same at every call.  The compiler knows that a branch on it has one active thread
+// and feeds the instructions that want uniform operands directly; under `lane == 0` it goes through the warp's
+// possible values for every operand, and an MMA took 95 clocks to issue, whatever its size.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, bf16: A's rows are TMEM lanes, a column holds two neighbouring K elements
+template <bool ACC>
+__device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "n"(ACC ? 1 : 0)
+        : "memory");
+}
+// one 16-column step of both operands
+template <bool ACC>
+__device__ __forceinline__ void mma_step(uint32_t d0, uint32_t d1, uint32_t a, uint64_t bd, uint32_t idesc) {
+    tc_mma_ta<ACC>(d0, a, bd, idesc);
+    tc_mma_ta<ACC>(d1, a + 32, bd, idesc);
+}
+
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+
+// What a group of a row needs, both halves alike.  Fast: w 2^-16 = fma(nibble in place, s0 or s1, c) with
+// s0 = s 2^117, s1 = s 2^113, c = -z s 2^-16.  Slow: (128 + q - z) s 2^-16 in two steps.
+struct Scale {
+    uint32_t s0, s1, c;  // slow: s 2^-16, unused, -(128 + z)
+};
+// the powers of two by exponent arithmetic: scales from 2^-103 to below 2^11 (others, 0 among them, are slow)
+template <bool ZERO>
+__device__ __forceinline__ bool fast_scale(uint32_t sbits) {
+    return ((sbits >> 7) & 255u) - 24u < 114u && (!ZERO || (sbits & 15u) == 0u);
+}
+template <bool ZERO>
+__device__ __forceinline__ Scale make_scale(uint32_t sbits, uint32_t zero, bool slow) {
+    Scale r;
+    const uint32_t s = sbits * 0x00010001u;
+    if (!slow) {
+        r.s0 = s + (117u << 7) * 0x00010001u;
+        r.s1 = s + (113u << 7) * 0x00010001u;
+        if (ZERO) {
+            const uint32_t one = 0xBF80BF80u, k128 = 0x43004300u, none = 0x80008000u;  // -1, 128, -0
+            r.c = fma2(fma2(k128 | zero * 0x00010001u, one, k128), s - (16u << 7) * 0x00010001u, none);
+        } else {
+            r.c = (s - (13u << 7) * 0x00010001u) ^ 0x80008000u;
+        }
+    } else {
+        const __nv_bfloat162 t = __float2bfloat162_rn(bf16_bits_to_f32(sbits) * 0x1p-16f);
+        r.s0 = *reinterpret_cast<const uint32_t*>(&t);
+        r.s1 = 0u;
+        r.c = 0xC3000000u + 0xC300u + (ZERO ? zero : 8u) * 0x00010001u;
+    }
+    return r;
+}
+// eight weights of a word: pairs of neighbouring columns
+__device__ __forceinline__ void unpack_fast(uint32_t w, const Scale& k, uint32_t* o) {
+    const uint32_t v = w >> 8;
+    o[0] = fma2(w & 0x000F000Fu, k.s0, k.c);
+    o[1] = fma2(w & 0x00F000F0u, k.s1, k.c);
+    o[2] = fma2(v & 0x000F000Fu, k.s0, k.c);
+    o[3] = fma2(v & 0x00F000F0u, k.s1, k.c);
+}
+__device__ __forceinline__ void unpack_slow(uint32_t w, const Scale& k, uint32_t* o) {
+    const uint32_t one = 0x3F803F80u, none = 0x80008000u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = fma2(fma2(((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u, one, k.c), k.s0, none);
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
+// GP: 32-column pieces of a group
+template <bool SWIGLU, int GP, bool ZERO>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_gemm_w4_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_q0,
+                           const __grid_constant__ CUtensorMap tm_q1, const __grid_constant__ CUtensorMap tm_s0,
+                           const __grid_constant__ CUtensorMap tm_s1, const __grid_constant__ CUtensorMap tm_z0,
+                           const __grid_constant__ CUtensorMap tm_z1, const Args p) {
+    constexpr int WROWS = SWIGLU ? 128 : 256;  // output features of a tile
+    constexpr int NG = 4 / GP;                 // groups of a stage
+    constexpr int kTx = 2 * (kOpBytes + NG * 256 + (ZERO ? NG * 128 : 0));
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int R = p.R, CS = p.cstages, XS = p.xstages;
+    const uint32_t x_bytes = R * 256;
+    uint8_t* xbase = smem + CS * kStageStride;
+    uint8_t* epi = xbase + XS * x_bytes;
+    Aux& aux = *reinterpret_cast<Aux*>(epi + kEpiBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* abort_flag = &aux.abort_flag;
+    const uint64_t wait_ns = p.wait_ns;
+    const int nbuf = R <= 64 ? 2 : 1;
+
+    if (warp == kProducer && lane == 0) {
+        for (int s = 0; s < kMaxStages; ++s) {
+            mbar_init(smem_u32(&aux.cfull[s]), 1);
+            mbar_init(smem_u32(&aux.cempty[s]), 16);
+            mbar_init(smem_u32(&aux.xfull[s]), 1);
+            mbar_init(smem_u32(&aux.xempty[s]), 1);
+        }
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(smem_u32(&aux.afull[s]), 8);
+            mbar_init(smem_u32(&aux.aempty[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&aux.tfull[s]), 1);
+            mbar_init(smem_u32(&aux.tempty[s]), 8);
+        }
+        mbar_init(smem_u32(&aux.drain), 1);
+        mbar_init(smem_u32(&aux.never), 1);
+        aux.abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch(&tm_x);
+        tma_prefetch(&tm_q0);
+        tma_prefetch(&tm_q1);
+        tma_prefetch(&tm_s0);
+        tma_prefetch(&tm_s1);
+        if (ZERO) {
+            tma_prefetch(&tm_z0);
+            tma_prefetch(&tm_z1);
+        }
+    }
+    if (warp == kIssuer) tmem_alloc(smem_u32(&aux.tmem_slot), 512);
+
+    pdl_wait();
+    const int E = p.E;
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+        int o, n;
+        if (!clamp_segment(p.offsets[e], p.counts[e], p.S, o, n)) set_status(p.status, DEV_BAD_COUNT);
+        aux.cnt[e] = n;
+        aux.off[e] = o;
+    }
+    __syncthreads();
+    const int ncb = (p.n_out + WROWS - 1) / WROWS;
+    if (warp == 0) {
+        int loc[8], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = lane * 8 + i;
+            loc[i] = (e < E) ? ((aux.cnt[e] + R - 1) / R) * ncb : 0;
+            sum += loc[i];
+        }
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += n;
+        }
+        int run = incl - sum;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = lane * 8 + i;
+            if (e < E) aux.tstart[e] = run;
+            run += loc[i];
+        }
+        if (lane == 31) aux.tstart[E] = incl;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_trigger();
+    const uint32_t tmem_base = aux.tmem_slot;
+    const int total = aux.tstart[E];
+    const int nk = (p.K + kCols - 1) / kCols;
+
+    auto give_up = [&]() {
+        if (lane == 0) {
+            *abort_flag = 1;
+            set_status(p.status, DEV_TIMEOUT);
+        }
+    };
+
+    if (warp == kProducer) {
+        // ================= TMA producer
+        int cs = 0, xs = 0;
+        uint32_t cph = 0, xph = 0, cused = 0, xused = 0, clast = 0, xlast = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; tile < total && ok && !*abort_flag; tile += gridDim.x) {
+            int e, rb, cb;
+            decode_tile(aux, E, R, tile, e, rb, cb);
+            const int w_row = e * p.n_out + cb * WROWS;
+            const int x_row = aux.off[e] + rb * R;
+            for (int kb = 0; kb < nk; ++kb) {
+                if (!quick_wait(smem_u32(&aux.cempty[cs]), cph ^ 1u, abort_flag, wait_ns)) {
+                    give_up();
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    const uint32_t full = smem_u32(&aux.cfull[cs]);
+                    const uint32_t q = smem_u32(smem + cs * kStageStride), s = q + 2 * kOpBytes, z = s + 2 * kScaleBytes;
+                    mbar_expect_tx(full, kTx);
+                    tma_load_2d(q, &tm_q0, kb * (kCols / 2), w_row, full);
+                    tma_load_2d(q + kOpBytes, &tm_q1, kb * (kCols / 2), SWIGLU ? w_row : w_row + 128, full);
+                    const int f0 = cb * WROWS, f1 = SWIGLU ? f0 : f0 + 128, gr = e * p.G + kb * NG;
+                    tma_load_2d(s, &tm_s0, f0, gr, full);
+                    tma_load_2d(s + kScaleBytes, &tm_s1, f1, gr, full);
+                    if (ZERO) {
+                        tma_load_2d(z, &tm_z0, f0, gr, full);
+                        tma_load_2d(z + kZeroBytes, &tm_z1, f1, gr, full);
+                    }
+                }
+                cused |= 1u << cs;
+                clast = (clast & ~(1u << cs)) | (cph << cs);
+                if (++cs == CS) {
+                    cs = 0;
+                    cph ^= 1u;
+                }
+                if (!quick_wait(smem_u32(&aux.xempty[xs]), xph ^ 1u, abort_flag, wait_ns)) {
+                    give_up();
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    const uint32_t full = smem_u32(&aux.xfull[xs]);
+                    const uint32_t x = smem_u32(xbase + xs * x_bytes);
+                    mbar_expect_tx(full, x_bytes);
+                    tma_load_2d(x, &tm_x, kb * kCols, x_row, full);
+                    tma_load_2d(x + R * 128, &tm_x, kb * kCols + 64, x_row, full);
+                }
+                xused |= 1u << xs;
+                xlast = (xlast & ~(1u << xs)) | (xph << xs);
+                if (++xs == XS) {
+                    xs = 0;
+                    xph ^= 1u;
+                }
+            }
+        }
+        const uint64_t dl = drain_deadline();
+        for (int s = 0; s < kMaxStages; ++s) {
+            if (cused & (1u << s)) mbar_drain(smem_u32(&aux.cfull[s]), (clast >> s) & 1u, dl);
+            if (xused & (1u << s)) mbar_drain(smem_u32(&aux.xfull[s]), (xlast >> s) & 1u, dl);
+        }
+    } else if (warp == kIssuer) {
+        // ================= MMA issuer
+        int xs = 0, slot = 0;
+        uint32_t xph = 0, sph = 0, j = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; tile < total && ok && !*abort_flag; tile += gridDim.x, ++j) {
+            int e, rb, cb;
+            decode_tile(aux, E, R, tile, e, rb, cb);
+            const int rows = min(R, aux.cnt[e] - rb * R);
+            const uint32_t idesc = idesc_bf16(128, (rows + 15) & ~15);
+            const uint32_t buf = nbuf == 2 ? (j & 1u) : 0u, use = nbuf == 2 ? j >> 1 : j;
+            const uint32_t d0 = tmem_base + buf * 128, d1 = d0 + (nbuf == 2 ? 64 : 128);
+            if (!quick_wait(smem_u32(&aux.tempty[buf]), (use & 1u) ^ 1u, abort_flag, wait_ns)) {
+                give_up();
+                break;
+            }
+            for (int kb = 0; kb < nk && ok; ++kb) {
+                if (!quick_wait(smem_u32(&aux.xfull[xs]), xph, abort_flag, wait_ns)) {
+                    give_up();
+                    ok = false;
+                    break;
+                }
+                const uint32_t x = smem_u32(xbase + xs * x_bytes);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!quick_wait(smem_u32(&aux.afull[slot]), sph, abort_flag, wait_ns)) {
+                        give_up();
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t a = tmem_base + 256 + slot * 64;
+                        const uint64_t bd = sdesc_sw128(x + h * R * 128);
+                        const int left = p.K - kb * kCols - h * 64;  // a multiple of 32
+                        if (left >= 64) {
+                            if (kb + h == 0) mma_step<false>(d0, d1, a, bd, idesc);
+                            else mma_step<true>(d0, d1, a, bd, idesc);
+#pragma unroll
+                            for (int kk = 1; kk < 4; ++kk) mma_step<true>(d0, d1, a + kk * 8, bd + kk * 2, idesc);
+                        } else if (left > 0) {
+                            if (kb + h == 0) mma_step<false>(d0, d1, a, bd, idesc);
+                            else mma_step<true>(d0, d1, a, bd, idesc);
+                            mma_step<true>(d0, d1, a + 8, bd + 2, idesc);
+                        }
+                        tc_commit(smem_u32(&aux.aempty[slot]));
+                        if (h == 1) tc_commit(smem_u32(&aux.xempty[xs]));
+                    }
+                    __syncwarp();
+                    if (++slot == kSlots) {
+                        slot = 0;
+                        sph ^= 1u;
+                    }
+                }
+                if (++xs == XS) {
+                    xs = 0;
+                    xph ^= 1u;
+                }
+            }
+            if (ok && elect_one()) tc_commit(smem_u32(&aux.tfull[buf]));
+            __syncwarp();
+        }
+        if (elect_one()) {
+            tc_commit(smem_u32(&aux.drain));
+            mbar_drain(smem_u32(&aux.drain), 0, drain_deadline());
+        }
+        __syncwarp();
+    } else if (warp < 16) {
+        // ================= unpack: a weight row per thread
+        const int qw = warp & 3, op = (warp >> 2) & 1, half = warp >> 3, row = 32 * qw + lane;
+        const uint32_t a_lane = tmem_base + 256 + op * 32 + ((uint32_t)(32 * qw) << 16);
+        const uint32_t swz = (uint32_t)((row >> 1) & 3);  // the 64-byte swizzle of the codes' rows
+        const uint32_t q0 = op * kOpBytes + row * 64, c0 = ((2u * half) ^ swz) << 4, c1 = ((2u * half + 1) ^ swz) << 4;
+        constexpr int NH = GP == 1 ? 2 : 1;  // groups of 64 columns
+        const int g0 = half * 2 / GP;        // the first of them in the stage
+        const int s_at = 2 * kOpBytes + op * kScaleBytes + g0 * 256 + row * 2;
+        const int z_at = 2 * kOpBytes + 2 * kScaleBytes + op * kZeroBytes + g0 * 128 + row;
+        int cs = 0, slot = half;
+        uint32_t cph = 0, sph = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; tile < total && ok && !*abort_flag; tile += gridDim.x) {
+            for (int kb = 0; kb < nk; ++kb) {
+                if (!quick_wait(smem_u32(&aux.cfull[cs]), cph, abort_flag, wait_ns)) {
+                    give_up();
+                    ok = false;
+                    break;
+                }
+                const uint8_t* st = smem + cs * kStageStride;
+                const uint4 w0 = *reinterpret_cast<const uint4*>(st + q0 + c0);
+                const uint4 w1 = *reinterpret_cast<const uint4*>(st + q0 + c1);
+                uint32_t sb[NH], zb[NH];
+                bool fast = true;
+#pragma unroll
+                for (int i = 0; i < NH; ++i) {
+                    sb[i] = *reinterpret_cast<const uint16_t*>(st + s_at + i * 256);
+                    zb[i] = ZERO ? st[z_at + i * 128] : 0u;
+                    fast = fast && fast_scale<ZERO>(sb[i]);
+                }
+                const bool slow = !__all_sync(0xffffffffu, fast);  // (every lane has read the stage)
+                if (lane == 0) mbar_arrive(smem_u32(&aux.cempty[cs]));
+                if (++cs == CS) {
+                    cs = 0;
+                    cph ^= 1u;
+                }
+                uint32_t o[32];
+                if (!slow) {
+                    Scale k[NH];
+#pragma unroll
+                    for (int i = 0; i < NH; ++i) k[i] = make_scale<ZERO>(sb[i], zb[i], false);
+                    unpack_fast(w0.x, k[0], o);
+                    unpack_fast(w0.y, k[0], o + 4);
+                    unpack_fast(w0.z, k[0], o + 8);
+                    unpack_fast(w0.w, k[0], o + 12);
+                    unpack_fast(w1.x, k[NH - 1], o + 16);
+                    unpack_fast(w1.y, k[NH - 1], o + 20);
+                    unpack_fast(w1.z, k[NH - 1], o + 24);
+                    unpack_fast(w1.w, k[NH - 1], o + 28);
+                } else {
+                    Scale k[NH];
+#pragma unroll
+                    for (int i = 0; i < NH; ++i) k[i] = make_scale<ZERO>(sb[i], zb[i], true);
+                    unpack_slow(w0.x, k[0], o);
+                    unpack_slow(w0.y, k[0], o + 4);
+                    unpack_slow(w0.z, k[0], o + 8);
+                    unpack_slow(w0.w, k[0], o + 12);
+                    unpack_slow(w1.x, k[NH - 1], o + 16);
+                    unpack_slow(w1.y, k[NH - 1], o + 20);
+                    unpack_slow(w1.z, k[NH - 1], o + 24);
+                    unpack_slow(w1.w, k[NH - 1], o + 28);
+                }
+                if (!quick_wait(smem_u32(&aux.aempty[slot]), sph ^ 1u, abort_flag, wait_ns)) {
+                    give_up();
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                tmem_st32(a_lane + slot * 64, o);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&aux.afull[slot]));
+                slot += 2;
+                if (slot >= kSlots) {
+                    slot = half;
+                    sph ^= 1u;
+                }
+            }
+        }
+    } else {
+        // ================= epilogue
+        const int qw = warp & 3, part = (warp - 16) >> 2;
+        const uint32_t stage = smem_u32(epi + (warp - 16) * 2048);
+        uint32_t j = 0;
+        bool ok = true;
+        if (p.stall && !quick_wait(smem_u32(&aux.never), 0, abort_flag, wait_ns)) {
+            give_up();
+            ok = false;
+        }
+        for (int tile = blockIdx.x; tile < total && ok && !*abort_flag; tile += gridDim.x, ++j) {
+            int e, rb, cb;
+            decode_tile(aux, E, R, tile, e, rb, cb);
+            const int rows = min(R, aux.cnt[e] - rb * R);
+            const int64_t base = aux.off[e] + rb * R;
+            const uint32_t buf = nbuf == 2 ? (j & 1u) : 0u, use = nbuf == 2 ? j >> 1 : j;
+            const uint32_t lanes = (uint32_t)(32 * qw) << 16;
+            const uint32_t d0 = tmem_base + buf * 128 + lanes, d1 = d0 + (nbuf == 2 ? 64 : 128);
+            if (!quick_wait(smem_u32(&aux.tfull[buf]), use & 1u, abort_flag, wait_ns)) {
+                give_up();
+                break;
+            }
+            tc_fence_after();
+            // this warp's 32 features; whole or not at all, as n_out is a multiple of 32
+            const int f0 = cb * WROWS + (SWIGLU ? 0 : 128 * part) + 32 * qw;
+            const bool live = f0 < p.n_out;
+            const int pieces = (rows + 31) >> 5;
+            // a piece: 32 token rows of the 32 features
+            for (int i = SWIGLU ? part : 0; i < pieces; i += SWIGLU ? 2 : 1) {
+                const int n = min(32, rows - 32 * i);
+                uint32_t b16[32];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (16 * half >= n) break;
+                    uint32_t g[16], u[16];
+                    const uint32_t at = 32 * i + 16 * half;
+                    tmem_ld16((SWIGLU || part == 0 ? d0 : d1) + at, g);
+                    if (SWIGLU) tmem_ld16(d1 + at, u);
+                    tmem_wait_ld(g);
+                    if (SWIGLU) tmem_wait_ld(u);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        float v = __uint_as_float(g[c]) * 65536.f;
+                        if (SWIGLU) v = __fdividef(v, 1.0f + __expf(-v)) * (__uint_as_float(u[c]) * 65536.f);
+                        b16[16 * half + c] = f32_to_bf16_bits(v);
+                    }
+                }
+                if (i + (SWIGLU ? 2 : 1) >= pieces) {  // the accumulator has been read
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&aux.tempty[buf]));
+                }
+                // transpose: token c's 32 features are 64 bytes
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    if (c < n) asm volatile("st.shared.b16 [%0], %1;" ::"r"(stage + c * 64 + lane * 2), "h"((uint16_t)b16[c]) : "memory");
+                __syncwarp();
+                if (live) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int tok = c * 8 + (lane >> 2);
+                        if (tok < n)
+                            st16(p.out + (base + 32 * i + tok) * p.n_out + f0 + (lane & 3) * 8,
+                                 lds16(stage + tok * 64 + (lane & 3) * 16));
+                    }
+                }
+                __syncwarp();
+            }
+            if (SWIGLU && part >= pieces) {  // no piece of this tile was this warp's
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&aux.tempty[buf]));
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kIssuer) tmem_dealloc(tmem_base, 512);
+}
+
+static bool encode(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t rows,
+                   uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz) {
+    EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {inner, rows};
+    cuuint64_t strides[1] = {row_bytes};
+    cuuint32_t box[2] = {box_inner, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(tm, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool SWIGLU, int GP, bool ZERO>
+static cudaError_t run(const Ctx& c, const void* x, const W4& w0, const W4& w1, Args a) {
+    set_wait_args(a);
+    auto kern = grouped_gemm_w4_kernel<SWIGLU, GP, ZERO>;
+    static bool attr_done[64] = {};
+    if (c.device < 0 || c.device >= 64) return cudaErrorInvalidDevice;
+    if (!attr_done[c.device]) {
+        cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+        if (err != cudaSuccess) return err;
+        attr_done[c.device] = true;
+    }
+    constexpr int WROWS = SWIGLU ? 128 : 256, NG = 4 / GP;
+    CUtensorMap tx, tq[2], ts[2], tz[2];
+    const uint64_t wrows = (uint64_t)a.E * a.n_out, grows = (uint64_t)a.E * a.G;
+    bool ok = encode(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, a.K, a.S, (uint64_t)a.K * 2, 64, a.R,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+    for (int i = 0; i < 2; ++i) {
+        const W4& w = i ? w1 : w0;
+        ok = ok && encode(&tq[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, w.q, a.K / 2, wrows, a.K / 2, kCols / 2, 128,
+                          CU_TENSOR_MAP_SWIZZLE_64B);
+        ok = ok && encode(&ts[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w.s, a.n_out, grows, (uint64_t)a.n_out * 2, 128, NG,
+                          CU_TENSOR_MAP_SWIZZLE_NONE);
+        if (ZERO)
+            ok = ok && encode(&tz[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, w.z, a.n_out, grows, a.n_out, 128, NG,
+                              CU_TENSOR_MAP_SWIZZLE_NONE);
+        else tz[i] = ts[i];
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    // shared memory: as many code stages as the latency wants, the rest token stages
+    const int left = kSmemLimit - 1024 - kAuxBytes - kEpiBytes;
+    a.cstages = a.R <= 64 ? 6 : 4;
+    a.xstages = (left - a.cstages * kStageStride) / (a.R * 256);
+    if (a.xstages > kMaxStages) a.xstages = kMaxStages;
+    if (a.xstages < 2) return cudaErrorInvalidValue;
+    const size_t smem = 1024 + (size_t)a.cstages * kStageStride + (size_t)a.xstages * a.R * 256 + kEpiBytes + kAuxBytes;
+    const int64_t max_tiles = ((int64_t)a.S / a.R + a.E) * ((a.n_out + WROWS - 1) / WROWS);
+    const int grid = (int)(max_tiles < c.num_sms ? max_tiles : c.num_sms);
+    if (grid <= 0) return cudaSuccess;
+    return launch(kern, dim3(grid), dim3(kThreads), smem, c, tx, tq[0], tq[1], ts[0], ts[1], tz[0], tz[1], a);
+}
+
+template <bool SWIGLU>
+static cudaError_t run_group(const Ctx& c, const void* x, const W4& w0, const W4& w1, int group, const Args& a) {
+    if (group == 32) return w0.z ? run<SWIGLU, 1, true>(c, x, w0, w1, a) : run<SWIGLU, 1, false>(c, x, w0, w1, a);
+    if (group == 64) return w0.z ? run<SWIGLU, 2, true>(c, x, w0, w1, a) : run<SWIGLU, 2, false>(c, x, w0, w1, a);
+    return w0.z ? run<SWIGLU, 4, true>(c, x, w0, w1, a) : run<SWIGLU, 4, false>(c, x, w0, w1, a);
+}
+
+// token rows per tile: the least of 16, 32, 64 and 128 that holds about twice an expert's average, so that few
+// experts need a second pass over their weights
+static int tile_rows(int S, int E) {
+    const int avg = S / E;
+    return avg <= 8 ? 16 : (avg <= 16 ? 32 : (avg <= 40 ? 64 : 128));
+}
+
+static Args base_args(const int32_t* counts, const int32_t* offsets, int S, int E, int K, int n_out, int group, void* out,
+                      int32_t* status) {
+    Args a{};
+    a.counts = counts;
+    a.offsets = offsets;
+    a.E = E;
+    a.K = K;
+    a.n_out = n_out;
+    a.G = (K + group - 1) / group;
+    a.R = tile_rows(S, E);
+    a.out = static_cast<uint16_t*>(out);
+    a.status = status;
+    a.S = S;
+    return a;
+}
+
+}  // namespace w4t
+
+cudaError_t launch_gate_up_w4_tc(const Ctx& c, const void* xp, const W4& Wg, const W4& Wu, int group,
+                                 const int32_t* counts, const int32_t* offsets, int S, int E, int d, int d_ff, void* h,
+                                 int32_t* status) {
+    if (S == 0) return cudaSuccess;
+    return w4t::run_group<true>(c, xp, Wg, Wu, group, w4t::base_args(counts, offsets, S, E, d, d_ff, group, h, status));
+}
+
+cudaError_t launch_down_w4_tc(const Ctx& c, const void* h, const W4& Wd, int group, const int32_t* counts,
+                              const int32_t* offsets, int S, int E, int d, int d_ff, void* y, int32_t* status) {
+    if (S == 0) return cudaSuccess;
+    return w4t::run_group<false>(c, h, Wd, Wd, group, w4t::base_args(counts, offsets, S, E, d_ff, d, group, y, status));
+}
+
+}  // namespace moe

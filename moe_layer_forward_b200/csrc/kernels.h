@@ -165,12 +165,22 @@ cudaError_t launch_down_w4_picks(const Ctx& c, const float* h, const W4& Wd, int
                                  int E, int d, int d_ff, float* y, bool exact, int32_t* status);
 // moe_forward_w4 takes that form: few tokens, so that experts have a row or two each
 inline bool w4_use_picks(int T, int k, int E) { return T * k <= 128 && (T <= 8 || T * k <= 2 * E); }
-// expert-contiguous rows; gather (gate/up): slot i reads row gather[i] of act_rows rows
+// expert-contiguous rows; few rows per expert take the weight stream (expert_w4.cu), which may read its rows through
+// a map (gather: slot i reads row gather[i] of act_rows rows), more the tcgen05 kernel (expert_w4_tc.cu)
+#ifndef W4FEW
+#define W4FEW 4
+#endif
+inline bool w4_few_rows(int S, int E) { return S <= W4FEW * E; }
 cudaError_t launch_gate_up_w4(const Ctx& c, const void* xp, const W4& Wg, const W4& Wu, int group, const int32_t* counts,
                               const int32_t* offsets, int S, int E, int d, int d_ff, void* h, int32_t* status,
                               const int32_t* gather = nullptr, int act_rows = 0);
 cudaError_t launch_down_w4(const Ctx& c, const void* h, const W4& Wd, int group, const int32_t* counts,
                            const int32_t* offsets, int S, int E, int d, int d_ff, void* y, int32_t* status);
+cudaError_t launch_gate_up_w4_tc(const Ctx& c, const void* xp, const W4& Wg, const W4& Wu, int group,
+                                 const int32_t* counts, const int32_t* offsets, int S, int E, int d, int d_ff, void* h,
+                                 int32_t* status);
+cudaError_t launch_down_w4_tc(const Ctx& c, const void* h, const W4& Wd, int group, const int32_t* counts,
+                              const int32_t* offsets, int S, int E, int d, int d_ff, void* y, int32_t* status);
 
 // ---- step 5: weighted un-permute + residual (combine.cu)
 cudaError_t launch_combine(const Ctx& c, const void* y, int y_dt, const int32_t* token_slot, const float* w,
