@@ -113,7 +113,7 @@ typedef struct {
 } moe_w4_t;
 
 /* 4-bit expert weights: W_gate and W_up (n = d_ff, k = d), W_down (n = d, k = d_ff), one group size (32, 64
- * or 128); W_gate and W_up both have zero points or neither has.  gamma, W_r and b as in moe_weights_t. */
+ * or 128); all three have zero points or none has.  gamma, W_r and b as in moe_weights_t. */
 typedef struct {
     const float* gamma;
     const float* W_r;

@@ -52,7 +52,9 @@ class MoeW4(ctypes.Structure):
 
 
 class MoeWeightsW4(ctypes.Structure):
-    _fields_ = [("gamma", _vp), ("W_r", _vp), ("b", _vp), ("W_gate", MoeW4), ("W_up", MoeW4), ("W_down", MoeW4),
+    # W_gate, W_up and W_down are a moe_w4_t each; flat, they are set in one go
+    _fields_ = [("gamma", _vp), ("W_r", _vp), ("b", _vp), ("gate_q", _vp), ("gate_s", _vp), ("gate_z", _vp),
+                ("up_q", _vp), ("up_s", _vp), ("up_z", _vp), ("down_q", _vp), ("down_s", _vp), ("down_z", _vp),
                 ("group", _i32)]
 
 
@@ -442,8 +444,8 @@ def _current_device(fn):
 
     @functools.wraps(fn)
     def call(first, *args, **kwargs):
-        dev = (first.q if isinstance(first, W4Weights) else first).device
-        if dev.type != "cuda" or dev.index == torch.cuda.current_device():
+        dev = (first.q if isinstance(first, W4Weights) else first).get_device()
+        if dev < 0 or dev == torch.cuda.current_device():
             return fn(first, *args, **kwargs)
         with torch.cuda.device(dev):
             return fn(first, *args, **kwargs)
@@ -451,48 +453,68 @@ def _current_device(fn):
     return call
 
 
-def _expect(name: str, t: torch.Tensor, shape, dtype, device) -> None:
+def _expect(name: str, t: torch.Tensor, shape, dtype, dev: int):
+    """The address of t, once it is a contiguous tensor of that shape and type on device number dev."""
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} is on {t.device}, expected CUDA device {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _w4(name: str, w: W4Weights, E: int, n: int, k: int, device) -> MoeW4:
-    G = -(-k // w.group)
-    _expect(name + ".q", w.q, (E, n, k // 2), torch.uint8, device)
-    _expect(name + ".s", w.s, (E, G, n), torch.bfloat16, device)
-    if w.z is not None:
-        _expect(name + ".z", w.z, (E, G, n), torch.uint8, device)
-    return MoeW4(_p(w.q), _p(w.s), _p(w.z))
+def _w4(name: str, w: W4Weights, E: int, n: int, k: int, dev: int):
+    """The addresses of a matrix's codes, scales and zero points, once they fit E x n x k."""
+    q, s, z, group = w
+    sizes = (E, -(-k // group), n)
+    return (_expect(name, q, (E, n, k // 2), torch.uint8, dev),
+            _expect(name, s, sizes, torch.bfloat16, dev),
+            None if z is None else _expect(name, z, sizes, torch.uint8, dev))
 
 
-def _w4_weights(gamma, W_r, b, Wg, Wu, Wd, E, d, d_ff, device) -> MoeWeightsW4:
+def _w4_weights(gamma, W_r, b, Wg, Wu, Wd, E, d, d_ff, dev) -> MoeWeightsW4:
     if not Wg.group == Wu.group == Wd.group:
         raise ValueError("W_gate, W_up and W_down must have one group size")
-    return MoeWeightsW4(_p(gamma), _p(W_r), _p(b), _w4("W_gate", Wg, E, d_ff, d, device),
-                        _w4("W_up", Wu, E, d_ff, d, device), _w4("W_down", Wd, E, d, d_ff, device), Wg.group)
+    return MoeWeightsW4(gamma, W_r, b, *_w4("W_gate", Wg, E, d_ff, d, dev), *_w4("W_up", Wu, E, d_ff, d, dev),
+                        *_w4("W_down", Wd, E, d, d_ff, dev), Wg.group)
 
 
-def _segments(counts, offsets, E, status, device) -> None:
-    _expect("counts", counts, (E,), torch.int32, device)
-    _expect("offsets", offsets, (E + 1,), torch.int32, device)
-    _status(status, device)
+def _segments(counts, offsets, E, dev):
+    return (_expect("counts", counts, (E,), torch.int32, dev), _expect("offsets", offsets, (E + 1,), torch.int32, dev))
 
 
-def _status(status, device) -> None:
-    if status is not None and (status.dtype != torch.int32 or status.numel() < 1 or status.device != device):
+def _status(status, dev):
+    if status is None:
+        return None
+    if status.dtype != torch.int32 or status.numel() < 1 or status.get_device() != dev:
         raise ValueError("dev_status must hold an int32 on the tensors' device")
+    return status.data_ptr()
+
+
+def _scratch(ws, need, dev):
+    """The workspace's tensor (allocated where the caller brings none), its address and its size."""
+    if ws is None:
+        ws = torch.empty(max(need(), 1), dtype=torch.uint8, device=torch.device("cuda", dev))
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous on CUDA device {dev}")
+    return ws, ws.data_ptr(), ctypes.c_size_t(ws.numel() * ws.element_size())
+
+
+def _raw_stream(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 @_current_device
 def moe_quantize_w4(W, w4: W4Weights) -> None:
     """Codes, scales and (unless w4.z is None) zero points of the matrices W [E][n][k] (f32 or bf16), into w4's tensors."""
     E, n, k = W.shape
-    o = _w4("w4", w4, E, n, k, W.device)
-    _check("moe_quantize_w4", _lib.moe_quantize_w4(_p(W), _dt(W), E, n, k, w4.group, o.q, o.s, o.z, _stream(W.device)))
+    dev = W.get_device()
+    x = _expect("W", W, (E, n, k), W.dtype, dev)
+    q, s, z = _w4("w4", w4, E, n, k, dev)
+    _check("moe_quantize_w4", _lib.moe_quantize_w4(x, _dt(W), E, n, k, w4.group, q, s, z, _raw_stream(dev)))
 
 
 def quantize_w4_weights(W, group: int = 128, zero: bool = False) -> W4Weights:
@@ -512,9 +534,11 @@ def quantize_w4_weights(W, group: int = 128, zero: bool = False) -> W4Weights:
 def moe_dequantize_w4(w4: W4Weights, out) -> None:
     """The weights [E][n][k] that w4 stands for, into out (f32 or bf16)."""
     E, n, k = out.shape
-    w = _w4("w4", w4, E, n, k, out.device)
-    _check("moe_dequantize_w4", _lib.moe_dequantize_w4(ctypes.byref(w), E, n, k, w4.group, _p(out), _dt(out),
-                                                       _stream(out.device)))
+    dev = out.get_device()
+    o = _expect("out", out, (E, n, k), out.dtype, dev)
+    w = MoeW4(*_w4("w4", w4, E, n, k, dev))
+    _check("moe_dequantize_w4", _lib.moe_dequantize_w4(ctypes.byref(w), E, n, k, w4.group, o, _dt(out),
+                                                       _raw_stream(dev)))
 
 
 @_current_device
@@ -522,16 +546,16 @@ def moe_expert_gate_up_w4(xp, Wg: W4Weights, Wu: W4Weights, counts, offsets, h, 
     """h = SiLU(xp W_gate^T) * (xp W_up^T) per expert segment, 4-bit weights."""
     S, d = xp.shape
     E, d_ff, _ = Wg.q.shape
-    dev = xp.device
-    _expect("xp", xp, (S, d), torch.bfloat16, dev)
-    _expect("h", h, (S, d_ff), torch.bfloat16, dev)
-    _segments(counts, offsets, E, dev_status, dev)
+    dev = xp.get_device()
+    x = _expect("xp", xp, (S, d), torch.bfloat16, dev)
+    o = _expect("h", h, (S, d_ff), torch.bfloat16, dev)
+    ct, off = _segments(counts, offsets, E, dev)
     if Wg.group != Wu.group:
         raise ValueError("W_gate and W_up must have one group size")
-    g, u = _w4("W_gate", Wg, E, d_ff, d, dev), _w4("W_up", Wu, E, d_ff, d, dev)
+    g, u = MoeW4(*_w4("W_gate", Wg, E, d_ff, d, dev)), MoeW4(*_w4("W_up", Wu, E, d_ff, d, dev))
     _check("moe_expert_gate_up_w4",
-           _lib.moe_expert_gate_up_w4(_p(xp), ctypes.byref(g), ctypes.byref(u), Wg.group, _p(counts), _p(offsets), S, E,
-                                      d, d_ff, _p(h), _p(dev_status), _stream(dev)))
+           _lib.moe_expert_gate_up_w4(x, ctypes.byref(g), ctypes.byref(u), Wg.group, ct, off, S, E, d, d_ff, o,
+                                      _status(dev_status, dev), _raw_stream(dev)))
 
 
 @_current_device
@@ -539,14 +563,14 @@ def moe_expert_down_w4(h, Wd: W4Weights, counts, offsets, y, dev_status=None) ->
     """y = h W_down^T per expert segment, 4-bit weights."""
     S, d_ff = h.shape
     E, d, _ = Wd.q.shape
-    dev = h.device
-    _expect("h", h, (S, d_ff), torch.bfloat16, dev)
-    _expect("y", y, (S, d), torch.bfloat16, dev)
-    _segments(counts, offsets, E, dev_status, dev)
-    w = _w4("W_down", Wd, E, d, d_ff, dev)
+    dev = h.get_device()
+    x = _expect("h", h, (S, d_ff), torch.bfloat16, dev)
+    o = _expect("y", y, (S, d), torch.bfloat16, dev)
+    ct, off = _segments(counts, offsets, E, dev)
+    w = MoeW4(*_w4("W_down", Wd, E, d, d_ff, dev))
     _check("moe_expert_down_w4",
-           _lib.moe_expert_down_w4(_p(h), ctypes.byref(w), Wd.group, _p(counts), _p(offsets), S, E, d, d_ff, _p(y),
-                                   _p(dev_status), _stream(dev)))
+           _lib.moe_expert_down_w4(x, ctypes.byref(w), Wd.group, ct, off, S, E, d, d_ff, o, _status(dev_status, dev),
+                                   _raw_stream(dev)))
 
 
 @_current_device
@@ -555,15 +579,15 @@ def moe_grouped_swiglu_w4(xp, Wg: W4Weights, Wu: W4Weights, Wd: W4Weights, count
     """The expert MLP over expert-contiguous rows with 4-bit weights: moe_expert_gate_up_w4, then moe_expert_down_w4."""
     S, d = xp.shape
     E, d_ff, _ = Wg.q.shape
-    dev = xp.device
-    _expect("xp", xp, (S, d), torch.bfloat16, dev)
-    _expect("h", h, (S, d_ff), torch.bfloat16, dev)
-    _expect("y", y, (S, d), torch.bfloat16, dev)
-    _segments(counts, offsets, E, dev_status, dev)
+    dev = xp.get_device()
+    x = _expect("xp", xp, (S, d), torch.bfloat16, dev)
+    hp = _expect("h", h, (S, d_ff), torch.bfloat16, dev)
+    o = _expect("y", y, (S, d), torch.bfloat16, dev)
+    ct, off = _segments(counts, offsets, E, dev)
     w = _w4_weights(None, None, None, Wg, Wu, Wd, E, d, d_ff, dev)
     _check("moe_grouped_swiglu_w4",
-           _lib.moe_grouped_swiglu_w4(_p(xp), ctypes.byref(w), _p(counts), _p(offsets), S, E, d, d_ff, _p(h), _p(y),
-                                      _p(dev_status), _stream(dev)))
+           _lib.moe_grouped_swiglu_w4(x, ctypes.byref(w), ct, off, S, E, d, d_ff, hp, o, _status(dev_status, dev),
+                                      _raw_stream(dev)))
 
 
 def picks_w4_workspace_bytes(v, Wg: W4Weights, Wd: W4Weights, topk_idx) -> int:
@@ -586,21 +610,17 @@ def moe_picks_swiglu_w4(v, Wg: W4Weights, Wu: W4Weights, Wd: W4Weights, topk_idx
     T, d = v.shape
     E, d_ff, _ = Wg.q.shape
     k = topk_idx.shape[1]
-    dev = v.device
-    _expect("v", v, (T, d), torch.bfloat16, dev)
-    _expect("topk_idx", topk_idx, (T, k), torch.int32, dev)
-    _expect("topk_w", topk_w, (T, k), torch.float32, dev)
-    _expect("residual", residual, (T, d), residual.dtype, dev)
-    _expect("out", out, (T, d), out.dtype, dev)
-    _status(dev_status, dev)
+    dev = v.get_device()
+    x = _expect("v", v, (T, d), torch.bfloat16, dev)
+    idx = _expect("topk_idx", topk_idx, (T, k), torch.int32, dev)
+    wt = _expect("topk_w", topk_w, (T, k), torch.float32, dev)
+    r = _expect("residual", residual, (T, d), residual.dtype, dev)
+    o = _expect("out", out, (T, d), out.dtype, dev)
     w = _w4_weights(None, None, None, Wg, Wu, Wd, E, d, d_ff, dev)
-    if ws is None:
-        ws = torch.empty(max(picks_w4_workspace_bytes(v, Wg, Wd, topk_idx), 1), dtype=torch.uint8, device=dev)
-    n = ctypes.c_size_t(ws.numel() * ws.element_size())
+    ws, wsp, n = _scratch(ws, lambda: picks_w4_workspace_bytes(v, Wg, Wd, topk_idx), dev)
     _check("moe_picks_swiglu_w4",
-           _lib.moe_picks_swiglu_w4(_p(v), ctypes.byref(w), _p(topk_idx), _p(topk_w), _p(residual), _dt(residual), T, k,
-                                    E, d, d_ff, _p(out), _dt(out), _p(ws), ctypes.byref(n), _p(dev_status),
-                                    _stream(dev)))
+           _lib.moe_picks_swiglu_w4(x, ctypes.byref(w), idx, wt, r, _dt(residual), T, k, E, d, d_ff, o, _dt(out), wsp,
+                                    ctypes.byref(n), _status(dev_status, dev), _raw_stream(dev)))
 
 
 def _shape_w4(x, Wg: W4Weights, out, top_k, eps) -> MoeShape:
@@ -627,22 +647,15 @@ def moe_forward_w4(x, gamma, W_r, b, Wg: W4Weights, Wu: W4Weights, Wd: W4Weights
     """out = x + MoE(RMSNorm(x)) with 4-bit experts."""
     T, d = x.shape
     E, d_ff, _ = Wg.q.shape
-    dev = x.device
-    _expect("out", out, (T, d), out.dtype, dev)
-    _expect("gamma", gamma, (d,), torch.float32, dev)
-    _expect("W_r", W_r, (E, d), torch.float32, dev)
-    _expect("b", b, (E,), torch.float32, dev)
-    for name, t, shape, dtype in (("topk_idx", topk_idx, (T, top_k), torch.int32),
-                                  ("topk_w", topk_w, (T, top_k), torch.float32),
-                                  ("logits", logits, (T, E), torch.float32)):
-        if t is not None:
-            _expect(name, t, shape, dtype, dev)
-    _status(dev_status, dev)
+    dev = x.get_device()
+    xp = _expect("x", x, (T, d), x.dtype, dev)
+    o = _expect("out", out, (T, d), out.dtype, dev)
+    w = _w4_weights(_expect("gamma", gamma, (d,), torch.float32, dev), _expect("W_r", W_r, (E, d), torch.float32, dev),
+                    _expect("b", b, (E,), torch.float32, dev), Wg, Wu, Wd, E, d, d_ff, dev)
+    idx = None if topk_idx is None else _expect("topk_idx", topk_idx, (T, top_k), torch.int32, dev)
+    wt = None if topk_w is None else _expect("topk_w", topk_w, (T, top_k), torch.float32, dev)
+    lg = None if logits is None else _expect("logits", logits, (T, E), torch.float32, dev)
     shp = _shape_w4(x, Wg, out, top_k, eps)
-    w = _w4_weights(gamma, W_r, b, Wg, Wu, Wd, E, d, d_ff, dev)
-    if ws is None:
-        ws = torch.empty(max(forward_w4_workspace_bytes(x, Wg, out, top_k, eps), 1), dtype=torch.uint8, device=dev)
-    n = ctypes.c_size_t(ws.numel() * ws.element_size())
-    _check("moe_forward_w4", _lib.moe_forward_w4(ctypes.byref(shp), ctypes.byref(w), _p(x), _p(out), _p(topk_idx),
-                                                 _p(topk_w), _p(logits), _p(ws), ctypes.byref(n), _p(dev_status),
-                                                 _stream(dev)))
+    ws, wsp, n = _scratch(ws, lambda: forward_w4_workspace_bytes(x, Wg, out, top_k, eps), dev)
+    _check("moe_forward_w4", _lib.moe_forward_w4(ctypes.byref(shp), ctypes.byref(w), xp, o, idx, wt, lg, wsp,
+                                                 ctypes.byref(n), _status(dev_status, dev), _raw_stream(dev)))

@@ -636,31 +636,28 @@ bool valid_w4(const moe_w4_t& w) { return w.q && w.s && aligned16(w.q) && aligne
 W4 to_w4(const moe_w4_t& w) { return W4{w.q, static_cast<const uint16_t*>(w.s), w.z}; }
 bool valid_gate_up(const moe_w4_t& g, const moe_w4_t& u) { return valid_w4(g) && valid_w4(u) && !g.z == !u.z; }
 
-// the intermediates of the expert MLP of few picks: h and y in fp32, the combine's slot map
+// all three matrices have zero points or none has
+bool valid_experts(const moe_weights_w4_t& w) {
+    return valid_gate_up(w.W_gate, w.W_up) && valid_w4(w.W_down) && !w.W_gate.z == !w.W_down.z;
+}
+
+// the intermediates of the expert MLP of few picks, in fp32
 struct PicksWs {
     float* h;
     float* y;
-    int32_t* slot;
 };
 PicksWs carve_picks(Carve& cv, int P, int d, int d_ff) {
     PicksWs w;
     w.h = static_cast<float*>(cv.take((size_t)P * d_ff * sizeof(float)));
     w.y = static_cast<float*>(cv.take((size_t)P * d * sizeof(float)));
-    w.slot = static_cast<int32_t*>(cv.take((size_t)P * sizeof(int32_t)));
     return w;
 }
 
 moe_status_t run_picks(const Ctx& c, const void* v, const moe_weights_w4_t* w, const int32_t* idx, const float* wgt,
                        const void* residual, moe_dtype_t r_dt, int T, int k, int E, int d, int d_ff, void* out,
                        moe_dtype_t out_dt, const PicksWs& ws, int32_t* dev_status) {
-    const bool exact = out_dt == MOE_F32;
-    moe_status_t st = cuda_status(launch_gate_up_w4_picks(c, v, to_w4(w->W_gate), to_w4(w->W_up), w->group, idx, T, k, E,
-                                                          d, d_ff, ws.h, ws.slot, exact, dev_status));
-    if (st != MOE_OK) return st;
-    st = cuda_status(launch_down_w4_picks(c, ws.h, to_w4(w->W_down), w->group, idx, T, k, E, d, d_ff, ws.y,
-                                          exact, dev_status));
-    if (st != MOE_OK) return st;
-    return cuda_status(launch_combine(c, ws.y, MOE_F32, ws.slot, wgt, residual, r_dt, T, d, k, out, out_dt));
+    return cuda_status(launch_picks_w4(c, v, to_w4(w->W_gate), to_w4(w->W_up), to_w4(w->W_down), w->group, idx, wgt,
+                                       residual, r_dt, T, k, E, d, d_ff, ws.h, ws.y, out, out_dt, dev_status));
 }
 
 }  // namespace
@@ -724,7 +721,7 @@ moe_status_t moe_grouped_swiglu_w4(const void* xp, const moe_weights_w4_t* w, co
     if (!w) return MOE_ERR_INVALID_ARG;
     moe_status_t st = check_w4_shape(S, E, d, d_ff, w->group);
     if (st != MOE_OK || S == 0) return st;
-    if (!valid_w4(w->W_down) || !y || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+    if (!valid_experts(*w) || !y || !aligned16(y)) return MOE_ERR_INVALID_ARG;
     st = moe_expert_gate_up_w4(xp, &w->W_gate, &w->W_up, w->group, counts, offsets, S, E, d, d_ff, h, dev_status, stream);
     if (st != MOE_OK) return st;
     return moe_expert_down_w4(h, &w->W_down, w->group, counts, offsets, S, E, d, d_ff, y, dev_status, stream);
@@ -745,7 +742,7 @@ moe_status_t moe_picks_swiglu_w4(const void* v, const moe_weights_w4_t* w, const
     if (st != MOE_OK || query || T == 0) return st;
     if (!v || !topk_idx || !topk_w || !residual || !out || !aligned16(v) || !aligned16(residual) || !aligned16(out))
         return MOE_ERR_INVALID_ARG;
-    if (!valid_gate_up(w->W_gate, w->W_up) || !valid_w4(w->W_down)) return MOE_ERR_INVALID_ARG;
+    if (!valid_experts(*w)) return MOE_ERR_INVALID_ARG;
     Ctx c;
     st = make_ctx(stream, c);
     if (st != MOE_OK) return st;
@@ -802,7 +799,7 @@ moe_status_t moe_forward_w4(const moe_shape_t* shape, const moe_weights_w4_t* w,
     if (T > 0) {
         if (!x || !out || !w->gamma || !w->W_r || !w->b) return MOE_ERR_INVALID_ARG;
         if (!aligned16(x) || !aligned16(out) || !aligned16(w->gamma) || !aligned16(w->W_r)) return MOE_ERR_INVALID_ARG;
-        if (!valid_gate_up(w->W_gate, w->W_up) || !valid_w4(w->W_down)) return MOE_ERR_INVALID_ARG;
+        if (!valid_experts(*w)) return MOE_ERR_INVALID_ARG;
     }
     if (dev_status) {
         st = cuda_status(cudaMemsetAsync(dev_status, 0, sizeof(int32_t), c.stream));

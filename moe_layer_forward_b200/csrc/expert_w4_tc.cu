@@ -17,15 +17,15 @@
 //
 // What bounds it: the codes' bytes up to about 65 rows per expert, the tensor cores above.
 //
-// Warp roles (1 CTA per SM, 832 threads):
+// Warp roles (1 CTA per SM, 864 threads):
 //   warps 0..15  unpack: warp w the TMEM lane quarter w % 4 of operand (w / 4) % 2, columns 64 (w / 8) .. + 63 of
-//                every stage, into a ring of four A slots (64 columns of both operands).  Sixteen, because a
+//                every stage, into one of two A slots (128 columns of both operands).  Sixteen, because a
 //                warp's chain (codes, scale, unpack, store, wait) is long and its work per stage short
 //   warps 16..23 epilogue: warp w the quarter w % 4; gate/up: the even or odd 32-row pieces of the tile, down: one
 //                of the two operands.  A piece is transposed through 2 KB of shared memory of the warp's own.
-//   warp 24      TMA producer: a ring of code stages (128 columns of both operands, scales, zero points) and one of
+//   warp 24, 25  TMA producers: a ring of code stages (128 columns of both operands, scales, zero points) and one of
 //                token stages (R rows x 128 columns)
-//   warp 25      owns the TMEM allocation; lane 0 issues the MMAs and commits
+//   warp 26      owns the TMEM allocation; lane 0 issues the MMAs and commits
 // Tensor memory: columns 0..255 accumulators (R <= 64: two buffers of gate | up, else one), 256..511 the A ring.
 // Every wait is bounded; a wait that gives up raises DEV_TIMEOUT and all roles unwind as in expert_tc.cu.
 #include <cuda.h>
@@ -39,8 +39,8 @@ namespace moe {
 namespace w4t {
 using namespace tc;
 
-constexpr int kThreads = 832;
-constexpr int kProducer = 24, kIssuer = 25;
+constexpr int kThreads = 864;
+constexpr int kCodeProducer = 24, kTokenProducer = 25, kIssuer = 26;
 constexpr int kSmemLimit = 232448;
 constexpr int kCols = 128;                    // columns of a stage
 constexpr int kOpBytes = 128 * (kCols / 2);   // codes of one operand's stage
@@ -49,7 +49,7 @@ constexpr int kZeroBytes = 4 * 128;
 constexpr int kStageBytes = 2 * (kOpBytes + kScaleBytes + kZeroBytes);
 constexpr int kStageStride = (kStageBytes + 1023) & ~1023;
 constexpr int kMaxStages = 8;
-constexpr int kSlots = 4;
+constexpr int kSlots = 2;
 constexpr int kEpiBytes = 8 * 2048;
 constexpr int kAuxBytes = 4096;
 
@@ -73,9 +73,8 @@ struct Aux {
     uint64_t cfull[kMaxStages];
     uint64_t cempty[kMaxStages];
     uint64_t xfull[kMaxStages];
-    uint64_t xempty[kMaxStages];
+    uint64_t done[kMaxStages];  // the stage's products are complete: its token rows and its A slot are free
     uint64_t afull[kSlots];
-    uint64_t aempty[kSlots];
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t drain;
@@ -143,7 +142,7 @@ __device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint
 template <bool ACC>
 __device__ __forceinline__ void mma_step(uint32_t d0, uint32_t d1, uint32_t a, uint64_t bd, uint32_t idesc) {
     tc_mma_ta<ACC>(d0, a, bd, idesc);
-    tc_mma_ta<ACC>(d1, a + 32, bd, idesc);
+    tc_mma_ta<ACC>(d1, a + 64, bd, idesc);
 }
 
 __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
@@ -225,16 +224,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t wait_ns = p.wait_ns;
     const int nbuf = R <= 64 ? 2 : 1;
 
-    if (warp == kProducer && lane == 0) {
+    if (warp == kCodeProducer && lane == 0) {
         for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(smem_u32(&aux.cfull[s]), 1);
             mbar_init(smem_u32(&aux.cempty[s]), 16);
             mbar_init(smem_u32(&aux.xfull[s]), 1);
-            mbar_init(smem_u32(&aux.xempty[s]), 1);
+            mbar_init(smem_u32(&aux.done[s]), 1);
         }
         for (int s = 0; s < kSlots; ++s) {
-            mbar_init(smem_u32(&aux.afull[s]), 8);
-            mbar_init(smem_u32(&aux.aempty[s]), 1);
+            mbar_init(smem_u32(&aux.afull[s]), 16);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&aux.tfull[s]), 1);
@@ -304,18 +302,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     };
 
-    if (warp == kProducer) {
-        // ================= TMA producer
-        int cs = 0, xs = 0;
-        uint32_t cph = 0, xph = 0, cused = 0, xused = 0, clast = 0, xlast = 0;
+    if (warp == kCodeProducer) {
+        // ================= TMA: codes, scales, zero points
+        int cs = 0;
+        uint32_t ph = 0, used = 0, last = 0;
         bool ok = true;
         for (int tile = blockIdx.x; tile < total && ok && !*abort_flag; tile += gridDim.x) {
             int e, rb, cb;
             decode_tile(aux, E, R, tile, e, rb, cb);
             const int w_row = e * p.n_out + cb * WROWS;
-            const int x_row = aux.off[e] + rb * R;
+            const int f0 = cb * WROWS, f1 = SWIGLU ? f0 : f0 + 128;
             for (int kb = 0; kb < nk; ++kb) {
-                if (!quick_wait(smem_u32(&aux.cempty[cs]), cph ^ 1u, abort_flag, wait_ns)) {
+                if (!quick_wait(smem_u32(&aux.cempty[cs]), ph ^ 1u, abort_flag, wait_ns)) {
                     give_up();
                     ok = false;
                     break;
@@ -323,10 +321,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elect_one()) {
                     const uint32_t full = smem_u32(&aux.cfull[cs]);
                     const uint32_t q = smem_u32(smem + cs * kStageStride), s = q + 2 * kOpBytes, z = s + 2 * kScaleBytes;
+                    const int gr = e * p.G + kb * NG;
                     mbar_expect_tx(full, kTx);
                     tma_load_2d(q, &tm_q0, kb * (kCols / 2), w_row, full);
                     tma_load_2d(q + kOpBytes, &tm_q1, kb * (kCols / 2), SWIGLU ? w_row : w_row + 128, full);
-                    const int f0 = cb * WROWS, f1 = SWIGLU ? f0 : f0 + 128, gr = e * p.G + kb * NG;
                     tma_load_2d(s, &tm_s0, f0, gr, full);
                     tma_load_2d(s + kScaleBytes, &tm_s1, f1, gr, full);
                     if (ZERO) {
@@ -334,13 +332,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_2d(z + kZeroBytes, &tm_z1, f1, gr, full);
                     }
                 }
-                cused |= 1u << cs;
-                clast = (clast & ~(1u << cs)) | (cph << cs);
+                __syncwarp();
+                used |= 1u << cs;
+                last = (last & ~(1u << cs)) | (ph << cs);
                 if (++cs == CS) {
                     cs = 0;
-                    cph ^= 1u;
+                    ph ^= 1u;
                 }
-                if (!quick_wait(smem_u32(&aux.xempty[xs]), xph ^ 1u, abort_flag, wait_ns)) {
+            }
+        }
+        const uint64_t dl = drain_deadline();
+        for (int s = 0; s < kMaxStages; ++s)
+            if (used & (1u << s)) mbar_drain(smem_u32(&aux.cfull[s]), (last >> s) & 1u, dl);
+    } else if (warp == kTokenProducer) {
+        // ================= TMA: token rows
+        int xs = 0;
+        uint32_t ph = 0, used = 0, last = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; tile < total && ok && !*abort_flag; tile += gridDim.x) {
+            int e, rb, cb;
+            decode_tile(aux, E, R, tile, e, rb, cb);
+            const int x_row = aux.off[e] + rb * R;
+            for (int kb = 0; kb < nk; ++kb) {
+                if (!quick_wait(smem_u32(&aux.done[xs]), ph ^ 1u, abort_flag, wait_ns)) {
                     give_up();
                     ok = false;
                     break;
@@ -352,19 +366,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_2d(x, &tm_x, kb * kCols, x_row, full);
                     tma_load_2d(x + R * 128, &tm_x, kb * kCols + 64, x_row, full);
                 }
-                xused |= 1u << xs;
-                xlast = (xlast & ~(1u << xs)) | (xph << xs);
+                __syncwarp();
+                used |= 1u << xs;
+                last = (last & ~(1u << xs)) | (ph << xs);
                 if (++xs == XS) {
                     xs = 0;
-                    xph ^= 1u;
+                    ph ^= 1u;
                 }
             }
         }
         const uint64_t dl = drain_deadline();
-        for (int s = 0; s < kMaxStages; ++s) {
-            if (cused & (1u << s)) mbar_drain(smem_u32(&aux.cfull[s]), (clast >> s) & 1u, dl);
-            if (xused & (1u << s)) mbar_drain(smem_u32(&aux.xfull[s]), (xlast >> s) & 1u, dl);
-        }
+        for (int s = 0; s < kMaxStages; ++s)
+            if (used & (1u << s)) mbar_drain(smem_u32(&aux.xfull[s]), (last >> s) & 1u, dl);
     } else if (warp == kIssuer) {
         // ================= MMA issuer
         int xs = 0, slot = 0;
@@ -387,37 +400,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                const uint32_t x = smem_u32(xbase + xs * x_bytes);
+                if (!quick_wait(smem_u32(&aux.afull[slot]), sph, abort_flag, wait_ns)) {
+                    give_up();
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t a = tmem_base + 256 + slot * 128;
+                    const uint32_t x = smem_u32(xbase + xs * x_bytes);
+                    const uint64_t b0 = sdesc_sw128(x), b1 = sdesc_sw128(x + R * 128);
+                    const int left = p.K - kb * kCols;  // a multiple of 32
+                    if (kb == 0) mma_step<false>(d0, d1, a, b0, idesc);
+                    else mma_step<true>(d0, d1, a, b0, idesc);
+                    mma_step<true>(d0, d1, a + 8, b0 + 2, idesc);
+                    if (left >= kCols) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!quick_wait(smem_u32(&aux.afull[slot]), sph, abort_flag, wait_ns)) {
-                        give_up();
-                        ok = false;
-                        break;
+                        for (int kk = 2; kk < 8; ++kk)
+                            mma_step<true>(d0, d1, a + kk * 8, (kk < 4 ? b0 : b1) + (kk & 3) * 2, idesc);
+                    } else {
+                        for (int kk = 2; kk < left / 16; ++kk)
+                            mma_step<true>(d0, d1, a + kk * 8, (kk < 4 ? b0 : b1) + (kk & 3) * 2, idesc);
                     }
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint32_t a = tmem_base + 256 + slot * 64;
-                        const uint64_t bd = sdesc_sw128(x + h * R * 128);
-                        const int left = p.K - kb * kCols - h * 64;  // a multiple of 32
-                        if (left >= 64) {
-                            if (kb + h == 0) mma_step<false>(d0, d1, a, bd, idesc);
-                            else mma_step<true>(d0, d1, a, bd, idesc);
-#pragma unroll
-                            for (int kk = 1; kk < 4; ++kk) mma_step<true>(d0, d1, a + kk * 8, bd + kk * 2, idesc);
-                        } else if (left > 0) {
-                            if (kb + h == 0) mma_step<false>(d0, d1, a, bd, idesc);
-                            else mma_step<true>(d0, d1, a, bd, idesc);
-                            mma_step<true>(d0, d1, a + 8, bd + 2, idesc);
-                        }
-                        tc_commit(smem_u32(&aux.aempty[slot]));
-                        if (h == 1) tc_commit(smem_u32(&aux.xempty[xs]));
-                    }
-                    __syncwarp();
-                    if (++slot == kSlots) {
-                        slot = 0;
-                        sph ^= 1u;
-                    }
+                    tc_commit(smem_u32(&aux.done[xs]));
+                }
+                __syncwarp();
+                if (++slot == kSlots) {
+                    slot = 0;
+                    sph ^= 1u;
                 }
                 if (++xs == XS) {
                     xs = 0;
@@ -435,15 +445,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < 16) {
         // ================= unpack: a weight row per thread
         const int qw = warp & 3, op = (warp >> 2) & 1, half = warp >> 3, row = 32 * qw + lane;
-        const uint32_t a_lane = tmem_base + 256 + op * 32 + ((uint32_t)(32 * qw) << 16);
+        const uint32_t a_lane = tmem_base + 256 + op * 64 + half * 32 + ((uint32_t)(32 * qw) << 16);
         const uint32_t swz = (uint32_t)((row >> 1) & 3);  // the 64-byte swizzle of the codes' rows
         const uint32_t q0 = op * kOpBytes + row * 64, c0 = ((2u * half) ^ swz) << 4, c1 = ((2u * half + 1) ^ swz) << 4;
         constexpr int NH = GP == 1 ? 2 : 1;  // groups of 64 columns
         const int g0 = half * 2 / GP;        // the first of them in the stage
         const int s_at = 2 * kOpBytes + op * kScaleBytes + g0 * 256 + row * 2;
         const int z_at = 2 * kOpBytes + 2 * kScaleBytes + op * kZeroBytes + g0 * 128 + row;
-        int cs = 0, slot = half;
-        uint32_t cph = 0, sph = 0;
+        int cs = 0, ds = 0;  // ds: the token stage of the products that free the slot, kSlots stages back
+        uint32_t cph = 0, dph = 0, j = 0;
         bool ok = true;
         for (int tile = blockIdx.x; tile < total && ok && !*abort_flag; tile += gridDim.x) {
             for (int kb = 0; kb < nk; ++kb) {
@@ -495,22 +505,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     unpack_slow(w1.z, k[NH - 1], o + 24);
                     unpack_slow(w1.w, k[NH - 1], o + 28);
                 }
-                if (!quick_wait(smem_u32(&aux.aempty[slot]), sph ^ 1u, abort_flag, wait_ns)) {
-                    give_up();
-                    ok = false;
-                    break;
+                if (j >= kSlots) {
+                    if (!quick_wait(smem_u32(&aux.done[ds]), dph, abort_flag, wait_ns)) {
+                        give_up();
+                        ok = false;
+                        break;
+                    }
+                    if (++ds == XS) {
+                        ds = 0;
+                        dph ^= 1u;
+                    }
                 }
+                const uint32_t slot = j++ % kSlots;
                 tc_fence_after();
-                tmem_st32(a_lane + slot * 64, o);
+                tmem_st32(a_lane + slot * 128, o);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&aux.afull[slot]));
-                slot += 2;
-                if (slot >= kSlots) {
-                    slot = half;
-                    sph ^= 1u;
-                }
             }
         }
     } else {

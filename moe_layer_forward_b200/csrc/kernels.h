@@ -52,6 +52,24 @@ cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
     return err;
 }
 
+// The same for a kernel whose CTAs wait for one another: the launch fails unless all of them can run at once.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cooperative(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, const Ctx& c, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = c.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+    if (err == cudaSuccess) g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
+    return err;
+}
+
 // ---- step 1: RMSNorm (norm_router.cu)
 cudaError_t launch_rmsnorm(const Ctx& c, const void* x, int x_dt, const float* gamma, int T, int d, float eps, void* v,
                            int v_dt, float* rstd);
@@ -156,13 +174,11 @@ cudaError_t launch_quant_w4(const Ctx& c, const void* x, int dt, int E, int64_t 
                             uint16_t* s, uint8_t* z);
 cudaError_t launch_dequant_w4(const Ctx& c, const uint8_t* q, const uint16_t* s, const uint8_t* z, int E, int64_t n, int k,
                               int group, void* out, int dt);
-// from the router's picks (T k <= 256): h [T k][d_ff] and y [T k][d] are fp32; slot gets the identity map for the
-// combine (-1 for a bad id); exact: the rows enter the products with 24 bits (else 16)
-cudaError_t launch_gate_up_w4_picks(const Ctx& c, const void* v, const W4& Wg, const W4& Wu, int group,
-                                    const int32_t* idx, int T, int k, int E, int d, int d_ff, float* h, int32_t* slot,
-                                    bool exact, int32_t* status);
-cudaError_t launch_down_w4_picks(const Ctx& c, const float* h, const W4& Wd, int group, const int32_t* idx, int T, int k,
-                                 int E, int d, int d_ff, float* y, bool exact, int32_t* status);
+// from the router's picks (T k <= 256), one cooperative launch: h [T k][d_ff] and y [T k][d] are fp32 workspaces; an
+// fp32 output takes the rows into the products with 24 bits (else 16)
+cudaError_t launch_picks_w4(const Ctx& c, const void* v, const W4& Wg, const W4& Wu, const W4& Wd, int group,
+                            const int32_t* idx, const float* w, const void* residual, int r_dt, int T, int k, int E, int d,
+                            int d_ff, float* h, float* y, void* out, int out_dt, int32_t* status);
 // moe_forward_w4 takes that form: few tokens, so that experts have a row or two each
 inline bool w4_use_picks(int T, int k, int E) { return T * k <= 128 && (T <= 8 || T * k <= 2 * E); }
 // expert-contiguous rows; few rows per expert take the weight stream (expert_w4.cu), which may read its rows through
