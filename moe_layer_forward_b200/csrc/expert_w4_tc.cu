@@ -18,9 +18,9 @@
 // What bounds it: the codes' bytes up to about 65 rows per expert, the tensor cores above.
 //
 // Warp roles (1 CTA per SM, 864 threads):
-//   warps 0..15  unpack: warp w the TMEM lane quarter w % 4 of operand (w / 4) % 2, columns 64 (w / 8) .. + 63 of
-//                every stage, into one of two A slots (128 columns of both operands).  Sixteen, because a
-//                warp's chain (codes, scale, unpack, store, wait) is long and its work per stage short
+//   warps 0..15  unpack: warps 0..7 the even stages into A slot 0, warps 8..15 the odd ones into slot 1 (128 columns of
+//                both operands); warp w the TMEM lane quarter w % 4 of operand (w / 4) % 2.  A stage's chain of
+//                waits, loads, arithmetic and stores is about two stages long, so two sets of warps keep up with it
 //   warps 16..23 epilogue: warp w the quarter w % 4; gate/up: the even or odd 32-row pieces of the tile, down: one
 //                of the two operands.  A piece is transposed through 2 KB of shared memory of the warp's own.
 //   warp 24, 25  TMA producers: a ring of code stages (128 columns of both operands, scales, zero points) and one of
@@ -227,12 +227,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kCodeProducer && lane == 0) {
         for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(smem_u32(&aux.cfull[s]), 1);
-            mbar_init(smem_u32(&aux.cempty[s]), 16);
+            mbar_init(smem_u32(&aux.cempty[s]), 8);
             mbar_init(smem_u32(&aux.xfull[s]), 1);
             mbar_init(smem_u32(&aux.done[s]), 1);
         }
         for (int s = 0; s < kSlots; ++s) {
-            mbar_init(smem_u32(&aux.afull[s]), 16);
+            mbar_init(smem_u32(&aux.afull[s]), 8);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&aux.tfull[s]), 1);
@@ -444,86 +444,79 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp < 16) {
         // ================= unpack: a weight row per thread
-        const int qw = warp & 3, op = (warp >> 2) & 1, half = warp >> 3, row = 32 * qw + lane;
-        const uint32_t a_lane = tmem_base + 256 + op * 64 + half * 32 + ((uint32_t)(32 * qw) << 16);
+        const int qw = warp & 3, op = (warp >> 2) & 1, slot = warp >> 3, row = 32 * qw + lane;
+        const uint32_t a_lane = tmem_base + 256 + slot * 128 + op * 64 + ((uint32_t)(32 * qw) << 16);
         const uint32_t swz = (uint32_t)((row >> 1) & 3);  // the 64-byte swizzle of the codes' rows
-        const uint32_t q0 = op * kOpBytes + row * 64, c0 = ((2u * half) ^ swz) << 4, c1 = ((2u * half + 1) ^ swz) << 4;
-        constexpr int NH = GP == 1 ? 2 : 1;  // groups of 64 columns
-        const int g0 = half * 2 / GP;        // the first of them in the stage
-        const int s_at = 2 * kOpBytes + op * kScaleBytes + g0 * 256 + row * 2;
-        const int z_at = 2 * kOpBytes + 2 * kScaleBytes + op * kZeroBytes + g0 * 128 + row;
-        int cs = 0, ds = 0;  // ds: the token stage of the products that free the slot, kSlots stages back
-        uint32_t cph = 0, dph = 0, j = 0;
-        bool ok = true;
-        for (int tile = blockIdx.x; tile < total && ok && !*abort_flag; tile += gridDim.x) {
-            for (int kb = 0; kb < nk; ++kb) {
-                if (!quick_wait(smem_u32(&aux.cfull[cs]), cph, abort_flag, wait_ns)) {
+        const uint32_t q0 = op * kOpBytes + row * 64;
+        const int s_at = 2 * kOpBytes + op * kScaleBytes + row * 2;
+        const int z_at = 2 * kOpBytes + 2 * kScaleBytes + op * kZeroBytes + row;
+        // this set's stages: slot, slot + 2, ...; ds: the token stage of the products before, which free the slot
+        int cs = slot, ds = slot;
+        uint32_t cph = 0, dph = 0;
+        const int ntiles = total > (int)blockIdx.x ? (total - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x : 0;
+        const int nstages = ntiles * nk;
+        for (int n = slot; n < nstages && !*abort_flag; n += kSlots) {
+            if (!quick_wait(smem_u32(&aux.cfull[cs]), cph, abort_flag, wait_ns)) {
+                give_up();
+                break;
+            }
+            const uint8_t* st = smem + cs * kStageStride;
+            uint4 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(st + q0 + ((i ^ swz) << 4));
+            uint32_t sb[NG], zb[NG];
+            bool fast = true;
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                sb[i] = *reinterpret_cast<const uint16_t*>(st + s_at + i * 256);
+                zb[i] = ZERO ? st[z_at + i * 128] : 0u;
+                fast = fast && fast_scale<ZERO>(sb[i]);
+            }
+            const bool slow = !__all_sync(0xffffffffu, fast);  // (every lane has read the stage)
+            if (lane == 0) mbar_arrive(smem_u32(&aux.cempty[cs]));
+            if ((cs += kSlots) >= CS) {
+                cs -= CS;
+                cph ^= 1u;
+            }
+            if (n >= kSlots) {
+                if (!quick_wait(smem_u32(&aux.done[ds]), dph, abort_flag, wait_ns)) {
                     give_up();
-                    ok = false;
                     break;
                 }
-                const uint8_t* st = smem + cs * kStageStride;
-                const uint4 w0 = *reinterpret_cast<const uint4*>(st + q0 + c0);
-                const uint4 w1 = *reinterpret_cast<const uint4*>(st + q0 + c1);
-                uint32_t sb[NH], zb[NH];
-                bool fast = true;
-#pragma unroll
-                for (int i = 0; i < NH; ++i) {
-                    sb[i] = *reinterpret_cast<const uint16_t*>(st + s_at + i * 256);
-                    zb[i] = ZERO ? st[z_at + i * 128] : 0u;
-                    fast = fast && fast_scale<ZERO>(sb[i]);
+                if ((ds += kSlots) >= XS) {
+                    ds -= XS;
+                    dph ^= 1u;
                 }
-                const bool slow = !__all_sync(0xffffffffu, fast);  // (every lane has read the stage)
-                if (lane == 0) mbar_arrive(smem_u32(&aux.cempty[cs]));
-                if (++cs == CS) {
-                    cs = 0;
-                    cph ^= 1u;
-                }
-                uint32_t o[32];
-                if (!slow) {
-                    Scale k[NH];
-#pragma unroll
-                    for (int i = 0; i < NH; ++i) k[i] = make_scale<ZERO>(sb[i], zb[i], false);
-                    unpack_fast(w0.x, k[0], o);
-                    unpack_fast(w0.y, k[0], o + 4);
-                    unpack_fast(w0.z, k[0], o + 8);
-                    unpack_fast(w0.w, k[0], o + 12);
-                    unpack_fast(w1.x, k[NH - 1], o + 16);
-                    unpack_fast(w1.y, k[NH - 1], o + 20);
-                    unpack_fast(w1.z, k[NH - 1], o + 24);
-                    unpack_fast(w1.w, k[NH - 1], o + 28);
-                } else {
-                    Scale k[NH];
-#pragma unroll
-                    for (int i = 0; i < NH; ++i) k[i] = make_scale<ZERO>(sb[i], zb[i], true);
-                    unpack_slow(w0.x, k[0], o);
-                    unpack_slow(w0.y, k[0], o + 4);
-                    unpack_slow(w0.z, k[0], o + 8);
-                    unpack_slow(w0.w, k[0], o + 12);
-                    unpack_slow(w1.x, k[NH - 1], o + 16);
-                    unpack_slow(w1.y, k[NH - 1], o + 20);
-                    unpack_slow(w1.z, k[NH - 1], o + 24);
-                    unpack_slow(w1.w, k[NH - 1], o + 28);
-                }
-                if (j >= kSlots) {
-                    if (!quick_wait(smem_u32(&aux.done[ds]), dph, abort_flag, wait_ns)) {
-                        give_up();
-                        ok = false;
-                        break;
-                    }
-                    if (++ds == XS) {
-                        ds = 0;
-                        dph ^= 1u;
-                    }
-                }
-                const uint32_t slot = j++ % kSlots;
-                tc_fence_after();
-                tmem_st32(a_lane + slot * 128, o);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&aux.afull[slot]));
             }
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t o[32];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int g = (2 * h + i) / GP;
+                    const uint4 c = w[2 * h + i];
+                    uint32_t* at = o + 16 * i;
+                    if (!slow) {
+                        const Scale k = make_scale<ZERO>(sb[g], zb[g], false);
+                        unpack_fast(c.x, k, at);
+                        unpack_fast(c.y, k, at + 4);
+                        unpack_fast(c.z, k, at + 8);
+                        unpack_fast(c.w, k, at + 12);
+                    } else {
+                        const Scale k = make_scale<ZERO>(sb[g], zb[g], true);
+                        unpack_slow(c.x, k, at);
+                        unpack_slow(c.y, k, at + 4);
+                        unpack_slow(c.z, k, at + 8);
+                        unpack_slow(c.w, k, at + 12);
+                    }
+                }
+                tmem_st32(a_lane + h * 32, o);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&aux.afull[slot]));
         }
     } else {
         // ================= epilogue
@@ -555,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // a piece: 32 token rows of the 32 features
             for (int i = SWIGLU ? part : 0; i < pieces; i += SWIGLU ? 2 : 1) {
                 const int n = min(32, rows - 32 * i);
-                uint32_t b16[32];
+                // transposed on the way: token c's 32 features are 64 bytes
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     if (16 * half >= n) break;
@@ -565,22 +558,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (SWIGLU) tmem_ld16(d1 + at, u);
                     tmem_wait_ld(g);
                     if (SWIGLU) tmem_wait_ld(u);
+                    if (i + (SWIGLU ? 2 : 1) >= pieces && 16 * half + 16 >= n) {  // the accumulator has been read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&aux.tempty[buf]));
+                    }
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
                         float v = __uint_as_float(g[c]) * 65536.f;
                         if (SWIGLU) v = __fdividef(v, 1.0f + __expf(-v)) * (__uint_as_float(u[c]) * 65536.f);
-                        b16[16 * half + c] = f32_to_bf16_bits(v);
+                        asm volatile("st.shared.b16 [%0], %1;" ::"r"(stage + (16 * half + c) * 64 + lane * 2),
+                                     "h"((uint16_t)f32_to_bf16_bits(v))
+                                     : "memory");
                     }
                 }
-                if (i + (SWIGLU ? 2 : 1) >= pieces) {  // the accumulator has been read
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&aux.tempty[buf]));
-                }
-                // transpose: token c's 32 features are 64 bytes
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    if (c < n) asm volatile("st.shared.b16 [%0], %1;" ::"r"(stage + c * 64 + lane * 2), "h"((uint16_t)b16[c]) : "memory");
                 __syncwarp();
                 if (live) {
 #pragma unroll
