@@ -72,9 +72,8 @@ struct Args {
 struct Aux {
     uint64_t cfull[kMaxStages];
     uint64_t cempty[kMaxStages];
-    uint64_t xfull[kMaxStages];
+    uint64_t ready[kMaxStages];  // the stage's token rows and its A slot are full (by token stage)
     uint64_t done[kMaxStages];  // the stage's products are complete: its token rows and its A slot are free
-    uint64_t afull[kSlots];
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t drain;
@@ -228,11 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(smem_u32(&aux.cfull[s]), 1);
             mbar_init(smem_u32(&aux.cempty[s]), 8);
-            mbar_init(smem_u32(&aux.xfull[s]), 1);
+            mbar_init(smem_u32(&aux.ready[s]), 9);  // the token TMA (with its bytes) + 8 unpacking warps
             mbar_init(smem_u32(&aux.done[s]), 1);
-        }
-        for (int s = 0; s < kSlots; ++s) {
-            mbar_init(smem_u32(&aux.afull[s]), 8);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&aux.tfull[s]), 1);
@@ -360,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 if (elect_one()) {
-                    const uint32_t full = smem_u32(&aux.xfull[xs]);
+                    const uint32_t full = smem_u32(&aux.ready[xs]);
                     const uint32_t x = smem_u32(xbase + xs * x_bytes);
                     mbar_expect_tx(full, x_bytes);
                     tma_load_2d(x, &tm_x, kb * kCols, x_row, full);
@@ -377,11 +373,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint64_t dl = drain_deadline();
         for (int s = 0; s < kMaxStages; ++s)
-            if (used & (1u << s)) mbar_drain(smem_u32(&aux.xfull[s]), (last >> s) & 1u, dl);
+            if (used & (1u << s)) mbar_drain(smem_u32(&aux.ready[s]), (last >> s) & 1u, dl);
     } else if (warp == kIssuer) {
         // ================= MMA issuer
-        int xs = 0, slot = 0;
-        uint32_t xph = 0, sph = 0, j = 0;
+        int xs = 0;
+        uint32_t xph = 0, slot = 0, j = 0;
         bool ok = true;
         for (int tile = blockIdx.x; tile < total && ok && !*abort_flag; tile += gridDim.x, ++j) {
             int e, rb, cb;
@@ -395,12 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             for (int kb = 0; kb < nk && ok; ++kb) {
-                if (!quick_wait(smem_u32(&aux.xfull[xs]), xph, abort_flag, wait_ns)) {
-                    give_up();
-                    ok = false;
-                    break;
-                }
-                if (!quick_wait(smem_u32(&aux.afull[slot]), sph, abort_flag, wait_ns)) {
+                if (!quick_wait(smem_u32(&aux.ready[xs]), xph, abort_flag, wait_ns)) {
                     give_up();
                     ok = false;
                     break;
@@ -425,10 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_commit(smem_u32(&aux.done[xs]));
                 }
                 __syncwarp();
-                if (++slot == kSlots) {
-                    slot = 0;
-                    sph ^= 1u;
-                }
+                slot ^= 1u;
                 if (++xs == XS) {
                     xs = 0;
                     xph ^= 1u;
@@ -451,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s_at = 2 * kOpBytes + op * kScaleBytes + row * 2;
         const int z_at = 2 * kOpBytes + 2 * kScaleBytes + op * kZeroBytes + row;
         // this set's stages: slot, slot + 2, ...; ds: the token stage of the products before, which free the slot
-        int cs = slot, ds = slot;
+        int cs = slot, ds = slot, xs = slot;
         uint32_t cph = 0, dph = 0;
         const int ntiles = total > (int)blockIdx.x ? (total - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x : 0;
         const int nstages = ntiles * nk;
@@ -488,6 +476,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     dph ^= 1u;
                 }
             }
+            const uint32_t ready = smem_u32(&aux.ready[xs]);
+            if ((xs += kSlots) >= XS) xs -= XS;
             tc_fence_after();
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -516,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&aux.afull[slot]));
+            if (lane == 0) mbar_arrive(ready);
         }
     } else {
         // ================= epilogue
