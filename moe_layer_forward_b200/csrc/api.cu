@@ -765,7 +765,7 @@ moe_status_t moe_forward_w4(const moe_shape_t* shape, const moe_weights_w4_t* w,
     st = make_ctx(stream, c);
     if (st != MOE_OK) return st;
     const RouterPlan plan = plan_router(T, d, E, c.num_sms);
-    const bool picks = w4_use_picks(T, k, E);
+    const bool picks = w4_use_picks(T, k, E, w->group);
 
     Carve cv(ws);
     void* v = cv.take((size_t)T * d * 2);
@@ -779,7 +779,7 @@ moe_status_t moe_forward_w4(const moe_shape_t* shape, const moe_weights_w4_t* w,
     PicksWs pw{};
     int32_t *hist = nullptr, *counts = nullptr, *offsets = nullptr, *slot_token = nullptr, *token_slot = nullptr;
     void *xp = nullptr, *h = nullptr, *y = nullptr;
-    const bool in_place = w4_few_rows(S, E);  // the weight stream reads the rows through slot_token
+    const bool in_place = w4_few_rows(S, E, w->group);  // the weight stream reads the rows through slot_token
     if (picks) {
         pw = carve_picks(cv, S, d, d_ff);
     } else {

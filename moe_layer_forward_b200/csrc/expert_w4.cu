@@ -48,11 +48,12 @@ constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 4;
 constexpr int kStageCols = 256;
-constexpr int kCodeBytes = 16 * (kStageCols / 2);            // 16 rows x 128 bytes
-constexpr int kScaleOff = kCodeBytes;                        // [group][16 rows] bf16
-constexpr int kZeroOff = kScaleOff + (kStageCols / 32) * 32; // [group][16 rows] u8
-constexpr int kStageBytes = kZeroOff + (kStageCols / 32) * 16;
-constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+// a warp's ring: kStages pieces of 16 rows x 128 bytes of codes; the scales and zero points of the same stages
+constexpr int kCodeBytes = 16 * (kStageCols / 2);
+constexpr int kZeroOff = (kStageCols / 32) * 32;              // [group][16 rows] bf16, then [group][16 rows] u8
+constexpr int kScaleBytes = kZeroOff + (kStageCols / 32) * 16;
+constexpr int kScales = kWarps * kStages * kCodeBytes;
+constexpr int kRingBytes = kScales + kWarps * kStages * kScaleBytes;
 constexpr int kSmemLimit = 232448;
 constexpr int kMaxPicks = 256;
 constexpr int kListed = 512;
@@ -233,7 +234,6 @@ __device__ __forceinline__ void stream(const Args& args, const Phase& p, uint8_t
     const int nstage = (p.K + kStageCols - 1) / kStageCols;
     const int pieces = p.K / 32;  // 32-column pieces of a row
     const int KP = p.G * GROUP;   // columns of a staged row: zeros past K
-    const uint32_t ring = smem_addr(smem) + warp * kStages * kStageBytes;
     const int g = lane >> 2, t = lane & 3;
 
     // expert and first row of chunk v
@@ -283,38 +283,40 @@ __device__ __forceinline__ void stream(const Args& args, const Phase& p, uint8_t
 
         // ---- this warp's units (base + warp, + kWarps, ...): the copies run kStages - 1 stages ahead
         int iu = base_u + warp, ist = 0, islot = 0;
-        const uint8_t *c0 = nullptr, *c1 = nullptr, *zp = nullptr;
+        // this lane's share of a stage: piece lane % 8 of rows lane / 8 + 4 j, and a scale and zero point piece
+        const uint8_t* src[4] = {};
+        const uint8_t* zp = nullptr;
         const uint16_t* sp = nullptr;
-        const uint32_t dst0 = ring + (lane >> 3) * 128;
+        const int r0 = lane >> 3;
+        uint32_t dst_c = smem_addr(smem) + warp * kStages * kCodeBytes + r0 * 128;
+        uint32_t dst_s = smem_addr(smem) + kScales + warp * kStages * kScaleBytes;
+        const uint32_t at0 = ((lane & 7) ^ ((r0 * GP) & 7)) << 4, at1 = at0 ^ (GP == 1 ? 64u : 0u);  // rows 4 j + r0: j even, odd
         auto issue_next = [&]() {
             if (iu < end_u) {
                 if (ist == 0) {
                     const int v = iu / nu, un = iu - v * nu;
                     const int64_t e = aux.be[v];
-                    const int64_t row = e * p.n_out + un * UROWS + (lane >> 3);
-                    c0 = p.q0 + row * (p.K / 2) + (lane & 7) * 16;
-                    c1 = (SWIGLU ? p.q1 + row * (p.K / 2) : p.q0 + (row + 8) * (p.K / 2)) + (lane & 7) * 16;
+                    const int64_t row = e * p.n_out + un * UROWS + r0;
+                    src[0] = p.q0 + row * (p.K / 2) + (lane & 7) * 16;
+                    src[2] = SWIGLU ? p.q1 + row * (p.K / 2) + (lane & 7) * 16 : src[0] + 4 * (int64_t)p.K;
+                    src[1] = src[0] + 2 * p.K;
+                    src[3] = src[2] + 2 * p.K;
                     const int64_t at = (e * p.G + (lane >> 1)) * p.n_out + un * UROWS + (SWIGLU ? 0 : 8 * (lane & 1));
                     sp = (SWIGLU && (lane & 1) ? p.s1 : p.s0) + at;
                     if (ZERO) zp = (SWIGLU && (lane & 1) ? p.z1 : p.z0) + at;
                 }
-                const uint32_t base = islot * kStageBytes;
                 if (ist * 8 + (lane & 7) < pieces) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int r = 4 * j + (lane >> 3);
-                        cp16(dst0 + base + j * 512 + (((lane & 7) ^ ((r * GP) & 7)) << 4),
-                             (j < 2 ? c0 : c1) + (j & 1) * 2 * p.K);
-                    }
+                    for (int j = 0; j < 4; ++j) cp16(dst_c + islot * kCodeBytes + j * 512 + (j & 1 ? at1 : at0), src[j]);
                 }
                 if (lane < 2 * NG && ist * NG + (lane >> 1) < p.G) {
-                    cp16(ring + base + kScaleOff + lane * 16, sp);
-                    if (ZERO) cp8(ring + base + kZeroOff + lane * 8, zp);
+                    cp16(dst_s + islot * kScaleBytes + lane * 16, sp);
+                    if (ZERO) cp8(dst_s + islot * kScaleBytes + kZeroOff + lane * 8, zp);
                 }
-                c0 += kStageCols / 2;
-                c1 += kStageCols / 2;
-                sp += (int64_t)NG * p.n_out;
-                if (ZERO) zp += (int64_t)NG * p.n_out;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) src[j] += kStageCols / 2;
+                sp += NG * p.n_out;
+                if (ZERO) zp += NG * p.n_out;
                 if (++islot == kStages) islot = 0;
                 if (++ist == nstage) {
                     ist = 0;
@@ -434,44 +436,45 @@ __device__ __forceinline__ void stream(const Args& args, const Phase& p, uint8_t
             float2 acc[2];
             acc[0] = acc[1] = make_float2(0.f, 0.f);
             // this lane's column of B and its two columns of the sums (rows past the chunk repeat others of it)
-            const uint8_t* xa = xs + (xrow + min(PACKED ? g % PR : g, n - 1)) * p.x_stride + t * (8 * GP) +
+            const uint8_t* xg = xs + (xrow + min(PACKED ? g % PR : g, n - 1)) * p.x_stride + t * (8 * GP) +
                                 (PACKED ? min(g / PR, TM - 1) * KP : 0);
-            const float* ma = meta + xrow + min(PACKED ? (2 * t) % PR : 2 * t, (n - 1) & ~1);
-            const float* mc = ma + (1 + (PACKED ? min(2 * t / PR, TM - 1) : 0)) * mplane;
+            const float* mg = meta + xrow + min(PACKED ? (2 * t) % PR : 2 * t, (n - 1) & ~1);
+            const int mc = (1 + (PACKED ? min(2 * t / PR, TM - 1) : 0)) * mplane;
             for (int st = 0; st < nstage; ++st) {
                 cp_wait<kStages - 2>();
                 __syncwarp();
-                const uint8_t* base = smem + (warp * kStages + slot) * kStageBytes;
+                // word t GP of group 0 of row g; other groups' pieces differ by an exclusive or, row g + 8 lies 1024 on
+                const int code_at = (warp * kStages + slot) * kCodeBytes + g * 128 +
+                                    ((((g * GP) & 7) ^ (t * GP / 4)) << 4) + (t * GP % 4) * 4;
+                const uint8_t* sc = smem + kScales + (warp * kStages + slot) * kScaleBytes;
                 auto do_group = [&](int gi) {
-                    const int gr = st * NG + gi;
                     uint32_t lo[GP], hi[GP];
-                    const int piece = (gi * GP) ^ ((g * GP) & 7);  // GP pieces share their upper bits with this one
+                    const uint8_t* codes = smem + (code_at ^ (gi * GP * 16));
                     if constexpr (GP == 4) {
-                        const uint4 a = *reinterpret_cast<const uint4*>(base + g * 128 + ((piece ^ t) << 4));
-                        const uint4 b = *reinterpret_cast<const uint4*>(base + (g + 8) * 128 + ((piece ^ t) << 4));
+                        const uint4 a = *reinterpret_cast<const uint4*>(codes);
+                        const uint4 b = *reinterpret_cast<const uint4*>(codes + 1024);
                         lo[0] = a.x; lo[1] = a.y; lo[2] = a.z; lo[3] = a.w;
                         hi[0] = b.x; hi[1] = b.y; hi[2] = b.z; hi[3] = b.w;
                     } else if constexpr (GP == 2) {
-                        const int at = ((piece ^ (t >> 1)) << 4) + (t & 1) * 8;
-                        const uint2 a = *reinterpret_cast<const uint2*>(base + g * 128 + at);
-                        const uint2 b = *reinterpret_cast<const uint2*>(base + (g + 8) * 128 + at);
+                        const uint2 a = *reinterpret_cast<const uint2*>(codes);
+                        const uint2 b = *reinterpret_cast<const uint2*>(codes + 1024);
                         lo[0] = a.x; lo[1] = a.y;
                         hi[0] = b.x; hi[1] = b.y;
                     } else {
-                        lo[0] = *reinterpret_cast<const uint32_t*>(base + g * 128 + (piece << 4) + t * 4);
-                        hi[0] = *reinterpret_cast<const uint32_t*>(base + (g + 8) * 128 + (piece << 4) + t * 4);
+                        lo[0] = *reinterpret_cast<const uint32_t*>(codes);
+                        hi[0] = *reinterpret_cast<const uint32_t*>(codes + 1024);
                     }
                     // the integer sums start at kMagic - z * (sum of the bytes): read as floats they are then
                     // 1.5 * 2^23 plus the group's sum, with no conversion
                     int part[BYTES][4];
                     int z_lo = 0, z_hi = 0;
                     if (ZERO) {
-                        z_lo = base[kZeroOff + gi * 16 + g];
-                        z_hi = base[kZeroOff + gi * 16 + 8 + g];
+                        z_lo = sc[kZeroOff + gi * 16 + g];
+                        z_hi = sc[kZeroOff + gi * 16 + 8 + g];
                     }
 #pragma unroll
                     for (int k = 0; k < BYTES; ++k) {
-                        const int2 m = *reinterpret_cast<const int2*>(mc + k * mplane + gr * mrows);
+                        const int2 m = *reinterpret_cast<const int2*>(mg + mc + k * mplane);
                         part[k][0] = ZERO ? kMagic - z_lo * m.x : m.x;
                         part[k][1] = ZERO ? kMagic - z_lo * m.y : m.y;
                         part[k][2] = ZERO ? kMagic - z_hi * m.x : m.x;
@@ -490,7 +493,7 @@ __device__ __forceinline__ void stream(const Args& args, const Phase& p, uint8_t
                         }
 #pragma unroll
                         for (int k = 0; k < BYTES; ++k) {
-                            const uint8_t* xp = xa + k * KP + gr * GROUP + w * 8;
+                            const uint8_t* xp = xg + k * KP + w * 8;
                             if constexpr (WI == 2) {
                                 const uint4 x = *reinterpret_cast<const uint4*>(xp);
                                 mma(part[k], a[0][0], a[0][1], a[0][2], a[0][3], x.x, x.y);
@@ -502,10 +505,10 @@ __device__ __forceinline__ void stream(const Args& args, const Phase& p, uint8_t
                         }
                     }
                     // ---- y += s / c * (P - z sum X)
-                    const uint16_t* ss = reinterpret_cast<const uint16_t*>(base + kScaleOff + gi * 32);
+                    const uint16_t* ss = reinterpret_cast<const uint16_t*>(sc + gi * 32);
                     const float s_lo = bf16_bits_to_f32(ss[g]), s_hi = bf16_bits_to_f32(ss[8 + g]);
                     const float2 magic = make_float2(-12582912.f, -12582912.f), k256 = make_float2(256.f, 256.f);
-                    const float2 inv = *reinterpret_cast<const float2*>(ma + gr * mrows);
+                    const float2 inv = *reinterpret_cast<const float2*>(mg);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float2 d = make_float2(0.f, 0.f);
@@ -515,9 +518,11 @@ __device__ __forceinline__ void stream(const Args& args, const Phase& p, uint8_t
                                 add2(make_float2(__int_as_float(part[k][2 * h]), __int_as_float(part[k][2 * h + 1])), magic);
                             d = k == BYTES - 1 ? f : fma2(d, k256, f);
                         }
-                        const float sc = h ? s_hi : s_lo;
-                        acc[h] = fma2(mul2(d, inv), make_float2(sc, sc), acc[h]);
+                        const float f = h ? s_hi : s_lo;
+                        acc[h] = fma2(mul2(d, inv), make_float2(f, f), acc[h]);
                     }
+                    xg += GROUP;
+                    mg += mrows;
                 };
                 if ((st + 1) * NG <= p.G) {
 #pragma unroll
@@ -781,7 +786,7 @@ cudaError_t launch_gate_up_w4(const Ctx& c, const void* xp, const W4& Wg, const 
                               const int32_t* offsets, int S, int E, int d, int d_ff, void* h, int32_t* status,
                               const int32_t* gather, int act_rows) {
     if (S == 0) return cudaSuccess;
-    if (!w4_few_rows(S, E)) {
+    if (!w4_few_rows(S, E, group)) {
         if (gather) return cudaErrorInvalidValue;
         return launch_gate_up_w4_tc(c, xp, Wg, Wu, group, counts, offsets, S, E, d, d_ff, h, status);
     }
@@ -795,7 +800,7 @@ cudaError_t launch_gate_up_w4(const Ctx& c, const void* xp, const W4& Wg, const 
 cudaError_t launch_down_w4(const Ctx& c, const void* h, const W4& Wd, int group, const int32_t* counts,
                            const int32_t* offsets, int S, int E, int d, int d_ff, void* y, int32_t* status) {
     if (S == 0) return cudaSuccess;
-    if (!w4_few_rows(S, E)) return launch_down_w4_tc(c, h, Wd, group, counts, offsets, S, E, d, d_ff, y, status);
+    if (!w4_few_rows(S, E, group)) return launch_down_w4_tc(c, h, Wd, group, counts, offsets, S, E, d, d_ff, y, status);
     w4s::Args a = w4s::segment_args(counts, offsets, S, E, status);
     a.ph[0] = w4s::phase(Wd, Wd, group, d_ff, d, h, y);
     return w4s::run_segments_group<false>(c, a, group);

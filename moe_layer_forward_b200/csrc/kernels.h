@@ -179,14 +179,14 @@ cudaError_t launch_dequant_w4(const Ctx& c, const uint8_t* q, const uint16_t* s,
 cudaError_t launch_picks_w4(const Ctx& c, const void* v, const W4& Wg, const W4& Wu, const W4& Wd, int group,
                             const int32_t* idx, const float* w, const void* residual, int r_dt, int T, int k, int E, int d,
                             int d_ff, float* h, float* y, void* out, int out_dt, int32_t* status);
-// moe_forward_w4 takes that form: few tokens, so that experts have a row or two each
-inline bool w4_use_picks(int T, int k, int E) { return T * k <= 128 && (T <= 8 || T * k <= 2 * E); }
-// expert-contiguous rows; few rows per expert take the weight stream (expert_w4.cu), which may read its rows through
-// a map (gather: slot i reads row gather[i] of act_rows rows), more the tcgen05 kernel (expert_w4_tc.cu)
-#ifndef W4FEW
-#define W4FEW 4
-#endif
-inline bool w4_few_rows(int S, int E) { return S <= W4FEW * E; }
+// Expert-contiguous rows: few rows per expert take the weight stream (expert_w4.cu), which may read its rows through
+// a map (gather: slot i reads row gather[i] of act_rows rows), more the tcgen05 kernel (expert_w4_tc.cu).  Measured
+// with 64 experts of 1536 x 4096, gate/up, stream against tcgen05: groups of 128 at 1 / 3 / 6 rows per expert 57 / 99
+// / 103 against 74 / 104 / 105 us; of 64 at 1 / 3 / 4 60 / 103 / 109 against 75 / 106 / 107 us; of 32 at 1 / 2 71 /
+// 112 against 78 / 94 us (the stream scales every group's sum, so fine groups cost it more).
+inline bool w4_few_rows(int S, int E, int group) { return S <= (group == 128 ? 6 : (group == 64 ? 3 : 1)) * E; }
+// moe_forward_w4 takes the picks form where it can and the weight stream is the one to take
+inline bool w4_use_picks(int T, int k, int E, int group) { return T * k <= 256 && w4_few_rows(T * k, E, group); }
 cudaError_t launch_gate_up_w4(const Ctx& c, const void* xp, const W4& Wg, const W4& Wu, int group, const int32_t* counts,
                               const int32_t* offsets, int S, int E, int d, int d_ff, void* h, int32_t* status,
                               const int32_t* gather = nullptr, int act_rows = 0);
