@@ -261,27 +261,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     const int ncb = (p.n_out + WROWS - 1) / WROWS;
     if (warp == 0) {
-        int loc[8], sum = 0;
+        int64_t loc[8], sum = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int e = lane * 8 + i;
-            loc[i] = (e < E) ? ((aux.cnt[e] + R - 1) / R) * ncb : 0;
+            loc[i] = (e < E) ? (int64_t)((aux.cnt[e] + R - 1) / R) * ncb : 0;
             sum += loc[i];
         }
-        int incl = sum;
+        int64_t incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int n = __shfl_up_sync(0xffffffffu, incl, o);
+            const int64_t n = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += n;
         }
-        int run = incl - sum;
+        int64_t run = incl - sum;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int e = lane * 8 + i;
-            if (e < E) aux.tstart[e] = run;
+            if (e < E) aux.tstart[e] = (int)run;
             run += loc[i];
         }
-        if (lane == 31) aux.tstart[E] = incl;
+        // segments that overlap so much that their tiles cannot be counted: nothing is computed
+        const bool many = incl > (int64_t(1) << 30);
+        if (lane == 31) {
+            aux.tstart[E] = many ? 0 : (int)incl;
+            if (many) set_status(p.status, DEV_BAD_COUNT);
+        }
     }
     tc_fence_before();
     __syncthreads();

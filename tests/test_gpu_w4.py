@@ -184,6 +184,86 @@ def test_grouped_wide_rows_take_several_passes(moe):
     assert any(right(*w) for w in ref.readings(Wg, Wu, Wd))
 
 
+@pytest.mark.parametrize("zero", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("counts", [[3, 2], [70, 200]])
+def test_grouped_scales_of_every_size(moe, counts, group, zero):
+    """Scales far from 1, of either sign, zero, and of many or few bits beside one another."""
+    gen = torch.Generator().manual_seed(group)
+    ct, off, S = segments(counts)
+    f, d = 416, 96
+    q, s, z, _ = weights(gen, 2, d, f, group, zero)
+    s = s.float()
+    s[0, 0, 0:8] = torch.tensor([2.0 ** 11, 2.0 ** 20, -3.0, 0.0, 2.0 ** -110, 2.0 ** -60, 1.9921875 * 2 ** 10, -0.0])
+    s[1] = (s[1].view(torch.int32) & ~0xFFFFF).view(F32)  # an expert whose scales have 4 significant bits
+    s[1, :, 5] = -s[1, :, 5]
+    Wd = (q, s.to(BF), z, group)
+    x = torch.randn((S, f), generator=gen).to(BF)
+    y = torch.empty((S, d), dtype=BF, device=DEV)
+    moe.moe_expert_down_w4(x.to(DEV), put(moe, Wd), ct.to(DEV), off.to(DEV), y)
+    y = y.cpu().double()
+
+    def right(w):
+        ok = True
+        for e, n in enumerate(counts):
+            o = int(off[e])
+            xr = x[o:o + n].double()
+            ok &= ref.within(y[o:o + n], xr @ w[e].T, ref.product_bound(xr, w[e], group), 2.0 ** -8)
+        return ok
+
+    assert any(right(*m) for m in ref.readings(Wd))
+
+
+def test_grouped_long_rows_many_of_them(moe):
+    gen = torch.Generator().manual_seed(15)
+    d, f, counts = 16384, 32, [40, 0, 90]
+    ct, off, S = segments(counts)
+    Wg, Wu = weights(gen, 3, f, d, 128, True), weights(gen, 3, f, d, 128, True)
+    x = torch.randn((S, d), generator=gen).to(BF)
+    h = torch.empty((S, f), dtype=BF, device=DEV)
+    moe.moe_expert_gate_up_w4(x.to(DEV), put(moe, Wg), put(moe, Wu), ct.to(DEV), off.to(DEV), h)
+    h = h.cpu().double()
+
+    def right(wg, wu):
+        ok = True
+        for e, n in enumerate(counts):
+            o = int(off[e])
+            if n:
+                hr, dh = ref.gate_up(x[o:o + n].double(), wg[e], wu[e], 128)
+                ok &= ref.within(h[o:o + n], hr, dh, 2.0 ** -8)
+        return ok
+
+    assert any(right(*m) for m in ref.readings(Wg, Wu))
+
+
+def test_grouped_waits_that_run_out(moe):
+    """As for the other tensor-core kernels: a stalled wait gives up, is reported, and the next call is right."""
+    gen = torch.Generator().manual_seed(16)
+    E, per, d, f = 4, 50, 256, 128
+    ct, off, S = segments([per] * E)
+    W = [put(moe, weights(gen, E, n, k, 64, True)) for n, k in ((f, d), (f, d), (d, f))]
+    x, ct, off = torch.randn((S, d), generator=gen).to(BF).to(DEV), ct.to(DEV), off.to(DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def call(st=None):
+        h, y = torch.zeros((S, f), dtype=BF, device=DEV), torch.zeros((S, d), dtype=BF, device=DEV)
+        moe.moe_grouped_swiglu_w4(x, *W, ct, off, h, y, dev_status=st)
+        return h, y
+
+    first = call()
+    torch.cuda.synchronize()
+    moe.set_wait_limit(2_000_000, inject_stall=True)
+    try:
+        call(status)
+    finally:
+        moe.set_wait_limit(0, inject_stall=False)
+    torch.cuda.synchronize()
+    assert status.item() & moe.MOE_DEV_TIMEOUT
+    again = call()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
 @pytest.mark.parametrize("counts", [[3, 5, 2, 9], [40, 150, 2, 300]])
 def test_grouped_rows_do_not_mix(moe, counts):
     """A row of NaN, infinities or huge values changes nothing but its own outputs; a NaN scale only its columns."""
