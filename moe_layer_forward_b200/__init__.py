@@ -455,15 +455,15 @@ def _current_device(fn):
 
 def _expect(name: str, t: torch.Tensor, shape, dtype, dev: int):
     """The address of t, once it is a contiguous tensor of that shape and type on device number dev."""
+    if t.shape == shape and t.dtype == dtype and t.get_device() == dev >= 0 and t.is_contiguous():
+        return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} is on {t.device}, expected CUDA device {dev}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, expected CUDA device {dev}")
 
 
 def _w4(name: str, w: W4Weights, E: int, n: int, k: int, dev: int):
@@ -503,8 +503,11 @@ def _scratch(ws, need, dev):
     return ws, ws.data_ptr(), ctypes.c_size_t(ws.numel() * ws.element_size())
 
 
-def _raw_stream(dev: int) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the current stream's handle without an object around it
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+else:
+    def _raw_stream(dev: int) -> int:
+        return torch.cuda.current_stream(dev).cuda_stream
 
 
 @_current_device
@@ -523,9 +526,8 @@ def quantize_w4_weights(W, group: int = 128, zero: bool = False) -> W4Weights:
     if group not in (32, 64, 128) or k % 32 != 0:
         raise ValueError("group must be 32, 64 or 128 and k a multiple of 32")
     G = -(-k // group)
-    w4 = W4Weights(torch.empty((E, n, k // 2), dtype=torch.uint8, device=W.device),
-                   torch.empty((E, G, n), dtype=torch.bfloat16, device=W.device),
-                   torch.empty((E, G, n), dtype=torch.uint8, device=W.device) if zero else None, group)
+    w4 = W4Weights(W.new_empty((E, n, k // 2), dtype=torch.uint8), W.new_empty((E, G, n), dtype=torch.bfloat16),
+                   W.new_empty((E, G, n), dtype=torch.uint8) if zero else None, group)
     moe_quantize_w4(W, w4)
     return w4
 
