@@ -621,26 +621,59 @@ __global__ void __launch_bounds__(kThreads, 1) picks_w4_kernel(const Args p) {
     namespace cg = cooperative_groups;
     const cg::grid_group grid = cg::this_grid();
 
-    // ---- which picks belong to which expert: a stable counting sort
-    for (int e = tid; e < p.E; e += kThreads) aux.cnt[e] = 0;
-    int my = -1, rank = 0;
-    if (tid < p.P) {
-        my = p.picks[tid];
-        if (my < 0 || my >= p.E) {
-            my = -1;
-            if (blockIdx.x == 0) set_status(p.status, DEV_BAD_EXPERT_ID);
+    // ---- which picks belong to which expert
+    if (p.P <= 32) {
+        // one warp: experts in the order of their first picks
+        if (tid < 32) {
+            const int id = tid < p.P ? p.picks[tid] : -1;
+            const bool ok = id >= 0 && id < p.E;
+            if (tid < p.P && !ok && blockIdx.x == 0) set_status(p.status, DEV_BAD_EXPERT_ID);
+            aux.id[tid] = (int16_t)(ok ? id : -1);
+            const uint32_t valid = __ballot_sync(0xffffffffu, ok);
+            const uint32_t peers = ok ? __match_any_sync(valid, id) : 1u << tid;
+            const int n = __popc(peers), lead = __ffs(peers) - 1;
+            const int chunks = (n + p.chunk_rows - 1) / p.chunk_rows;
+            const int own = ok && lead == tid ? n + (chunks << 16) : 0;  // rows, and chunks above them
+            int incl = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int m = __shfl_up_sync(0xffffffffu, incl, o);
+                if (tid >= o) incl += m;
+            }
+            const int before = __shfl_sync(0xffffffffu, incl - own, lead);
+            const int row = before & 0xFFFF, v = before >> 16;
+            if (ok) aux.order[row + __popc(peers & ((1u << tid) - 1u))] = (int16_t)tid;
+            if (own) {
+                aux.off[id] = row;
+                aux.cnt[id] = n;
+                aux.vstart[id] = v;
+                for (int c = 0; c < chunks; ++c) aux.chunk_e[v + c] = (uint8_t)id;
+            }
+            if (tid == 31) aux.vstart[p.E] = incl >> 16;
         }
-        aux.id[tid] = (int16_t)my;
+        __syncthreads();
+    } else {
+        // a stable counting sort
+        for (int e = tid; e < p.E; e += kThreads) aux.cnt[e] = 0;
+        int my = -1, rank = 0;
+        if (tid < p.P) {
+            my = p.picks[tid];
+            if (my < 0 || my >= p.E) {
+                my = -1;
+                if (blockIdx.x == 0) set_status(p.status, DEV_BAD_EXPERT_ID);
+            }
+            aux.id[tid] = (int16_t)my;
+        }
+        __syncthreads();
+        if (my >= 0) {
+            for (int o = 0; o < tid; ++o) rank += aux.id[o] == my;
+            atomicAdd(&aux.cnt[my], 1);
+        }
+        __syncthreads();
+        if (tid < 32) expert_prefixes<true>(aux, p.E, p.chunk_rows, tid);
+        __syncthreads();
+        if (my >= 0) aux.order[aux.off[my] + rank] = (int16_t)tid;
     }
-    __syncthreads();
-    if (my >= 0) {
-        for (int o = 0; o < tid; ++o) rank += aux.id[o] == my;
-        atomicAdd(&aux.cnt[my], 1);
-    }
-    __syncthreads();
-    if (tid < 32) expert_prefixes<true>(aux, p.E, p.chunk_rows, tid);
-    __syncthreads();
-    if (my >= 0) aux.order[aux.off[my] + rank] = (int16_t)tid;
 
     stream<true, true, TM, GP, ZERO>(p, p.ph[0], smem, [] {});
     stream<false, true, TM, GP, ZERO>(p, p.ph[1], smem, [&] { grid.sync(); });

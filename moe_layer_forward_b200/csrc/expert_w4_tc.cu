@@ -12,8 +12,8 @@
 // q 2^-133 in bits 0..3 and q 2^-129 in bits 4..7, so one packed FMA does the rest:
 //   w 2^-16 = q 2^-133 * (s 2^117) - z s 2^-16
 // It rounds once, and the last term is exact for z = 8 or scales of at most 4 significant bits, the quantiser's.
-// Other scales with zero points, and scales of 2^11 or more (s 2^117 would overflow), take 128 + q, a subtraction
-// and a product.  The epilogue multiplies the 2^16 back.
+// Other scales with zero points, and scales of 2^11 or more (s 2^117 would overflow) or below 2^-103 (0 among them),
+// take 128 + q, a subtraction and a product.  The epilogue multiplies the 2^16 back.
 //
 // What bounds it: the codes' bytes up to about 65 rows per expert, the tensor cores above.
 //

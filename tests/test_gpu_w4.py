@@ -541,16 +541,18 @@ def test_forward_on_another_stream_and_captured(moe, T):
     assert torch.equal(out, replayed) and not torch.equal(out, want)
 
 
-def test_two_calls_at_once_with_their_own_workspaces(moe):
+@pytest.mark.parametrize("tokens", [(3, 200), (2, 3), (1, 8, 60, 300)])
+def test_calls_at_once_with_their_own_workspaces(moe, tokens):
+    """Several streams; the form for few tokens, whose CTAs wait for one another, among them and beside itself."""
     gen = torch.Generator().manual_seed(21)
-    calls = [_layer_call(moe, gen, T, 256, 12, 128, 4) for T in (3, 200)]
+    calls = [_layer_call(moe, gen, T, 256, 12, 128, 4) for T in tokens]
     ws = [torch.empty(c[2], dtype=torch.uint8, device=DEV) for c in calls]
     want = []
     for c, w in zip(calls, ws):
         c[3](w)
         want.append(c[1].clone())
     torch.cuda.synchronize()
-    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    streams = [torch.cuda.Stream() for _ in tokens]
     for _ in range(10):
         for c, w, s in zip(calls, ws, streams):
             with torch.cuda.stream(s):
