@@ -58,8 +58,7 @@ struct Args {
     const int32_t* offsets;
     int E, K, n_out, G;
     int R;        // token rows per tile: 16, 32, 64 or 128
-    int cstages;  // code stages
-    int xstages;  // token stages
+    int stages;  // of the code ring and of the token ring
     uint16_t* out;
     int32_t* status;
     int S;  // rows of the expert-contiguous buffers; a segment that does not fit is clamped and flagged
@@ -213,10 +212,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kTx = 2 * (kOpBytes + NG * 256 + (ZERO ? NG * 128 : 0));
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int R = p.R, CS = p.cstages, XS = p.xstages;
+    const int R = p.R, NS = p.stages;
     const uint32_t x_bytes = R * 256;
-    uint8_t* xbase = smem + CS * kStageStride;
-    uint8_t* epi = xbase + XS * x_bytes;
+    uint8_t* xbase = smem + NS * kStageStride;
+    uint8_t* epi = xbase + NS * x_bytes;
     Aux& aux = *reinterpret_cast<Aux*>(epi + kEpiBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int* abort_flag = &aux.abort_flag;
@@ -336,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 used |= 1u << cs;
                 last = (last & ~(1u << cs)) | (ph << cs);
-                if (++cs == CS) {
+                if (++cs == NS) {
                     cs = 0;
                     ph ^= 1u;
                 }
@@ -370,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 used |= 1u << xs;
                 last = (last & ~(1u << xs)) | (ph << xs);
-                if (++xs == XS) {
+                if (++xs == NS) {
                     xs = 0;
                     ph ^= 1u;
                 }
@@ -422,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 slot ^= 1u;
-                if (++xs == XS) {
+                if (++xs == NS) {
                     xs = 0;
                     xph ^= 1u;
                 }
@@ -439,79 +438,84 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ================= unpack: a weight row per thread
         const int qw = warp & 3, op = (warp >> 2) & 1, slot = warp >> 3, row = 32 * qw + lane;
         const uint32_t a_lane = tmem_base + 256 + slot * 128 + op * 64 + ((uint32_t)(32 * qw) << 16);
-        const uint32_t swz = (uint32_t)((row >> 1) & 3);  // the 64-byte swizzle of the codes' rows
-        const uint32_t q0 = op * kOpBytes + row * 64;
-        const int s_at = 2 * kOpBytes + op * kScaleBytes + row * 2;
-        const int z_at = 2 * kOpBytes + 2 * kScaleBytes + op * kZeroBytes + row;
-        // this set's stages: slot, slot + 2, ...; ds: the token stage of the products before, which free the slot
-        int cs = slot, ds = slot, xs = slot;
-        uint32_t cph = 0, dph = 0;
+        // piece 0 of this row's codes under the 64-byte swizzle; the others differ by an exclusive or
+        const uint32_t codes = smem_u32(smem) + op * kOpBytes + row * 64 + (((row >> 1) & 3) << 4);
+        const uint8_t* scales = smem + 2 * kOpBytes + op * kScaleBytes + row * 2;
+        const uint8_t* zeros = smem + 2 * kOpBytes + 2 * kScaleBytes + op * kZeroBytes + row;
         const int ntiles = total > (int)blockIdx.x ? (total - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x : 0;
         const int nstages = ntiles * nk;
+        // this set's stages: slot, slot + 2, ...; the products of the one before free the slot
+        int cs = slot, before = 0;
+        uint32_t ph = 0, ph_before = 0;
         for (int n = slot; n < nstages && !*abort_flag; n += kSlots) {
-            if (!quick_wait(smem_u32(&aux.cfull[cs]), cph, abort_flag, wait_ns)) {
+            if (!quick_wait(smem_u32(&aux.cfull[cs]), ph, abort_flag, wait_ns)) {
                 give_up();
                 break;
             }
-            const uint8_t* st = smem + cs * kStageStride;
+            const int st = cs * kStageStride;
             uint4 w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(st + q0 + ((i ^ swz) << 4));
+            for (int i = 0; i < 4; ++i) w[i] = lds16((codes + st) ^ (i << 4));
             uint32_t sb[NG], zb[NG];
             bool fast = true;
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
-                sb[i] = *reinterpret_cast<const uint16_t*>(st + s_at + i * 256);
-                zb[i] = ZERO ? st[z_at + i * 128] : 0u;
+                sb[i] = *reinterpret_cast<const uint16_t*>(scales + st + i * 256);
+                zb[i] = ZERO ? zeros[st + i * 128] : 0u;
                 fast = fast && fast_scale<ZERO>(sb[i]);
             }
-            const bool slow = !__all_sync(0xffffffffu, fast);  // (every lane has read the stage)
+            const bool all_fast = __all_sync(0xffffffffu, fast);  // (every lane has read the stage)
             if (lane == 0) mbar_arrive(smem_u32(&aux.cempty[cs]));
-            if ((cs += kSlots) >= CS) {
-                cs -= CS;
-                cph ^= 1u;
+            if (n >= kSlots && !quick_wait(smem_u32(&aux.done[before]), ph_before, abort_flag, wait_ns)) {
+                give_up();
+                break;
             }
-            if (n >= kSlots) {
-                if (!quick_wait(smem_u32(&aux.done[ds]), dph, abort_flag, wait_ns)) {
-                    give_up();
-                    break;
-                }
-                if ((ds += kSlots) >= XS) {
-                    ds -= XS;
-                    dph ^= 1u;
-                }
-            }
-            const uint32_t ready = smem_u32(&aux.ready[xs]);
-            if ((xs += kSlots) >= XS) xs -= XS;
             tc_fence_after();
+            if (all_fast) {
+                Scale k[NG];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t o[32];
+                for (int i = 0; i < NG; ++i) k[i] = make_scale<ZERO>(sb[i], zb[i], false);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int g = (2 * h + i) / GP;
-                    const uint4 c = w[2 * h + i];
-                    uint32_t* at = o + 16 * i;
-                    if (!slow) {
-                        const Scale k = make_scale<ZERO>(sb[g], zb[g], false);
-                        unpack_fast(c.x, k, at);
-                        unpack_fast(c.y, k, at + 4);
-                        unpack_fast(c.z, k, at + 8);
-                        unpack_fast(c.w, k, at + 12);
-                    } else {
-                        const Scale k = make_scale<ZERO>(sb[g], zb[g], true);
-                        unpack_slow(c.x, k, at);
-                        unpack_slow(c.y, k, at + 4);
-                        unpack_slow(c.z, k, at + 8);
-                        unpack_slow(c.w, k, at + 12);
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t o[32];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 c = w[2 * h + i];
+                        const Scale& g = k[(2 * h + i) / GP];
+                        unpack_fast(c.x, g, o + 16 * i);
+                        unpack_fast(c.y, g, o + 16 * i + 4);
+                        unpack_fast(c.z, g, o + 16 * i + 8);
+                        unpack_fast(c.w, g, o + 16 * i + 12);
                     }
+                    tmem_st32(a_lane + h * 32, o);
                 }
-                tmem_st32(a_lane + h * 32, o);
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t o[32];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 c = w[2 * h + i];
+                        const int at = (2 * h + i) / GP;
+                        const Scale g = make_scale<ZERO>(sb[at], zb[at], true);
+                        unpack_slow(c.x, g, o + 16 * i);
+                        unpack_slow(c.y, g, o + 16 * i + 4);
+                        unpack_slow(c.z, g, o + 16 * i + 8);
+                        unpack_slow(c.w, g, o + 16 * i + 12);
+                    }
+                    tmem_st32(a_lane + h * 32, o);
+                }
             }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(ready);
+            if (lane == 0) mbar_arrive(smem_u32(&aux.ready[cs]));
+            before = cs;
+            ph_before = ph;
+            if ((cs += kSlots) >= NS) {
+                cs -= NS;
+                ph ^= 1u;
+            }
         }
     } else {
         // ================= epilogue
@@ -633,13 +637,11 @@ static cudaError_t run(const Ctx& c, const void* x, const W4& w0, const W4& w1, 
         else tz[i] = ts[i];
     }
     if (!ok) return cudaErrorInvalidValue;
-    // shared memory: as many code stages as the latency wants, the rest token stages
-    const int left = kSmemLimit - 1024 - kAuxBytes - kEpiBytes;
-    a.cstages = a.R <= 64 ? 6 : 4;
-    a.xstages = (left - a.cstages * kStageStride) / (a.R * 256);
-    if (a.xstages > kMaxStages) a.xstages = kMaxStages;
-    if (a.xstages < 2) return cudaErrorInvalidValue;
-    const size_t smem = 1024 + (size_t)a.cstages * kStageStride + (size_t)a.xstages * a.R * 256 + kEpiBytes + kAuxBytes;
+    // as many stages of codes and token rows as fit (4 at 128 token rows)
+    const int left = kSmemLimit - 1024 - kAuxBytes - kEpiBytes, stage = kStageStride + a.R * 256;
+    a.stages = left / stage < kMaxStages ? left / stage : kMaxStages;
+    static_assert((kSmemLimit - 1024 - kAuxBytes - kEpiBytes) / (kStageStride + 128 * 256) >= kSlots, "stages");
+    const size_t smem = 1024 + (size_t)a.stages * stage + kEpiBytes + kAuxBytes;
     const int64_t max_tiles = ((int64_t)a.S / a.R + a.E) * ((a.n_out + WROWS - 1) / WROWS);
     const int grid = (int)(max_tiles < c.num_sms ? max_tiles : c.num_sms);
     if (grid <= 0) return cudaSuccess;
