@@ -85,7 +85,10 @@ struct Aux {
 };
 static_assert(sizeof(Aux) <= kAuxBytes, "aux block");
 
-__device__ __forceinline__ void decode_tile(const Aux& a, int E, int R, int tile, int& e, int& rb, int& cb) {
+// Tile -> expert, first row and rows inside its segment, column block.  An expert's rows are cut evenly (in 16s)
+// over its ceil(cnt / R) blocks, since a block of few rows costs no less than its weights' unpacking: 130 rows are 80
+// and 50, not 128 and 2.  (No block is empty: where the even share is below R - 15 there are at most R / 16 blocks.)
+__device__ __forceinline__ void decode_tile(const Aux& a, int E, int R, int tile, int& e, int& first, int& rows, int& cb) {
     int lo = 0, hi = E - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -94,8 +97,10 @@ __device__ __forceinline__ void decode_tile(const Aux& a, int E, int R, int tile
     e = lo;
     const int local = tile - a.tstart[e];
     const int nrb = (a.cnt[e] + R - 1) / R;
+    const int per = ((a.cnt[e] + nrb - 1) / nrb + 15) & ~15;
     cb = local / nrb;
-    rb = local - cb * nrb;
+    first = (local - cb * nrb) * per;
+    rows = min(per, a.cnt[e] - first);
 }
 
 // mbar_wait with the timer read late: the roles here hand over every 64 columns, most waits are short but fail their
@@ -308,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t ph = 0, used = 0, last = 0;
         bool ok = true;
         for (int tile = blockIdx.x; tile < total && ok && !*abort_flag; tile += gridDim.x) {
-            int e, rb, cb;
-            decode_tile(aux, E, R, tile, e, rb, cb);
+            int e, first, rows, cb;
+            decode_tile(aux, E, R, tile, e, first, rows, cb);
             const int w_row = e * p.n_out + cb * WROWS;
             const int f0 = cb * WROWS, f1 = SWIGLU ? f0 : f0 + 128;
             for (int kb = 0; kb < nk; ++kb) {
@@ -350,9 +355,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t ph = 0, used = 0, last = 0;
         bool ok = true;
         for (int tile = blockIdx.x; tile < total && ok && !*abort_flag; tile += gridDim.x) {
-            int e, rb, cb;
-            decode_tile(aux, E, R, tile, e, rb, cb);
-            const int x_row = aux.off[e] + rb * R;
+            int e, first, rows, cb;
+            decode_tile(aux, E, R, tile, e, first, rows, cb);
+            const int x_row = aux.off[e] + first;
             for (int kb = 0; kb < nk; ++kb) {
                 if (!quick_wait(smem_u32(&aux.done[xs]), ph ^ 1u, abort_flag, wait_ns)) {
                     give_up();
@@ -384,9 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t xph = 0, slot = 0, j = 0;
         bool ok = true;
         for (int tile = blockIdx.x; tile < total && ok && !*abort_flag; tile += gridDim.x, ++j) {
-            int e, rb, cb;
-            decode_tile(aux, E, R, tile, e, rb, cb);
-            const int rows = min(R, aux.cnt[e] - rb * R);
+            int e, first, rows, cb;
+            decode_tile(aux, E, R, tile, e, first, rows, cb);
             const uint32_t idesc = idesc_bf16(128, (rows + 15) & ~15);
             const uint32_t buf = nbuf == 2 ? (j & 1u) : 0u, use = nbuf == 2 ? j >> 1 : j;
             const uint32_t d0 = tmem_base + buf * 128, d1 = d0 + (nbuf == 2 ? 64 : 128);
@@ -528,10 +532,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
         }
         for (int tile = blockIdx.x; tile < total && ok && !*abort_flag; tile += gridDim.x, ++j) {
-            int e, rb, cb;
-            decode_tile(aux, E, R, tile, e, rb, cb);
-            const int rows = min(R, aux.cnt[e] - rb * R);
-            const int64_t base = aux.off[e] + rb * R;
+            int e, first, rows, cb;
+            decode_tile(aux, E, R, tile, e, first, rows, cb);
+            const int64_t base = aux.off[e] + first;
             const uint32_t buf = nbuf == 2 ? (j & 1u) : 0u, use = nbuf == 2 ? j >> 1 : j;
             const uint32_t lanes = (uint32_t)(32 * qw) << 16;
             const uint32_t d0 = tmem_base + buf * 128 + lanes, d1 = d0 + (nbuf == 2 ? 64 : 128);

@@ -27,7 +27,7 @@ namespace w4 {
 
 constexpr int kWarps = 8;   // rows of a CTA
 constexpr int kCols = 256;  // columns of a piece: a word (8 columns) per lane
-constexpr int kAhead = 4;
+constexpr int kAhead = 4;  // pieces in flight
 
 // Offset by 0x4B400000: rint(x / s) exactly, ties to even.  half_bits: those of s / 2.
 __device__ __forceinline__ int round_quotient(float x, float s, float inv, uint32_t half_bits) {
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(32 * kWarps) quantize_w4_kernel(const void* __
     const int lane = threadIdx.x & 31;
     const int64_t e = blockIdx.y, row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (row >= n) return;
-    const int lanes = group >> 3;  // lanes of a group
+    const int lanes = group >> 3, lg = __ffs(group) - 1;  // lanes of a group; its size is a power of two
     const int64_t in = (e * n + row) * k;
     uint32_t* out = q + (in >> 3);
     for (int c0 = 8 * lane; c0 < k + 8 * lane; c0 += kAhead * kCols) {
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(32 * kWarps) quantize_w4_kernel(const void* __
             if (col < k) {
                 out[col >> 3] = word;
                 if ((lane & (lanes - 1)) == 0) {
-                    const int64_t at = (e * G + col / group) * n + row;
+                    const int64_t at = (e * G + (col >> lg)) * n + row;
                     // a value that is not finite (or >= 2^120) makes its group's scale NaN: it shows in every product
                     s[at] = finite ? (uint16_t)f32_to_bf16_bits(sc) : (uint16_t)0x7FC0u;
                     if (ZERO) z[at] = (uint8_t)zp;
@@ -136,34 +136,38 @@ __global__ void __launch_bounds__(32 * kWarps) dequantize_w4_kernel(const uint32
     const int64_t e = blockIdx.y, row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (row >= n) return;
     const int64_t at0 = (e * n + row) * k;
-    for (int c0 = 8 * lane; c0 < k; c0 += kAhead * kCols) {
+    const int lg = __ffs(group) - 1;
+    constexpr int C = DT == DT_F32 ? 4 : 8;  // columns of a lane: 16 bytes of output, so that a warp's stores are whole lines
+    for (int c0 = C * lane; c0 < k; c0 += kAhead * 32 * C) {
         uint32_t word[kAhead];
         uint16_t sc[kAhead];
         uint8_t zp[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int col = c0 + i * kCols;
+            const int col = c0 + i * 32 * C;
             word[i] = 0;
             sc[i] = 0;
             zp[i] = 8;
             if (col < k) {
-                word[i] = __ldg(q + ((at0 + col) >> 3));
-                const int64_t at = (e * G + col / group) * n + row;
+                word[i] = __ldg(q + ((at0 + col) >> 3)) >> (col & 4 ? 8 : 0);  // (columns 4..7 lie 8 bits on)
+                const int64_t at = (e * G + (col >> lg)) * n + row;
                 sc[i] = __ldg(s + at);
                 if (ZERO) zp[i] = __ldg(z + at);
             }
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int col = c0 + i * kCols;
+            const int col = c0 + i * 32 * C;
             if (col >= k) break;
             // 2^23 + code has the code in its low bits
             const float f = bf16_bits_to_f32(sc[i]), base = 8388608.f + (float)zp[i];
-            float v[8];
+            float v[C];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < C; ++j)
                 v[j] = (__uint_as_float(0x4B000000u | ((word[i] >> (4 * (j / 2 + 4 * (j & 1)))) & 15u)) - base) * f;
-            store8<DT>(out, at0 + col, v);
+            if constexpr (C == 4)
+                *reinterpret_cast<float4*>(static_cast<float*>(out) + at0 + col) = make_float4(v[0], v[1], v[2], v[3]);
+            else store8<DT>(out, at0 + col, v);
         }
     }
 }
