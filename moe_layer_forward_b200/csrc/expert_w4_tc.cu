@@ -26,7 +26,9 @@
 //   warp 24, 25  TMA producers: a ring of code stages (128 columns of both operands, scales, zero points) and one of
 //                token stages (R rows x 128 columns)
 //   warp 26      owns the TMEM allocation; lane 0 issues the MMAs and commits
-// Tensor memory: columns 0..255 accumulators (R <= 64: two buffers of gate | up, else one), 256..511 the A ring.
+// Tensor memory: columns 0..255 accumulators (R <= 64: two buffers of gate | up, else one), 256..511 the A slots.  Wide
+// tiles (192 rows): 384 columns of accumulators, and slots of 64 columns of both operands: their token ring and
+// their A slots turn in half stages.
 // Every wait is bounded; a wait that gives up raises DEV_TIMEOUT and all roles unwind as in expert_tc.cu.
 #include <cuda.h>
 #include <math.h>
@@ -50,6 +52,8 @@ constexpr int kStageBytes = 2 * (kOpBytes + kScaleBytes + kZeroBytes);
 constexpr int kStageStride = (kStageBytes + 1023) & ~1023;
 constexpr int kMaxStages = 8;
 constexpr int kSlots = 2;
+constexpr int kWideRows = 192;
+constexpr int kHalves = 4;  // token half stages of wide tiles: those of two stages, two to an unpacking set
 constexpr int kEpiBytes = 8 * 2048;
 constexpr int kAuxBytes = 4096;
 
@@ -57,8 +61,8 @@ struct Args {
     const int32_t* counts;
     const int32_t* offsets;
     int E, K, n_out, G;
-    int R;        // token rows per tile: 16, 32, 64 or 128
-    int stages;  // of the code ring and of the token ring
+    int R;        // token rows per tile: 16, 32, 64, 128 or kWideRows
+    int stages;  // of the code ring (and of the token ring but for wide tiles, whose token ring has kHalves)
     uint16_t* out;
     int32_t* status;
     int S;  // rows of the expert-contiguous buffers; a segment that does not fit is clamped and flagged
@@ -141,11 +145,11 @@ __device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "n"(ACC ? 1 : 0)
         : "memory");
 }
-// one 16-column step of both operands
-template <bool ACC>
+// one 16-column step of both operands, whose A columns are OP apart
+template <bool ACC, int OP>
 __device__ __forceinline__ void mma_step(uint32_t d0, uint32_t d1, uint32_t a, uint64_t bd, uint32_t idesc) {
     tc_mma_ta<ACC>(d0, a, bd, idesc);
-    tc_mma_ta<ACC>(d1, a + 64, bd, idesc);
+    tc_mma_ta<ACC>(d1, a + OP, bd, idesc);
 }
 
 __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
@@ -205,8 +209,8 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
     return v;
 }
 
-// GP: 32-column pieces of a group
-template <bool SWIGLU, int GP, bool ZERO>
+// GP: 32-column pieces of a group.  WIDE: tiles of up to 192 token rows.
+template <bool SWIGLU, int GP, bool ZERO, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_w4_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_q0,
                            const __grid_constant__ CUtensorMap tm_q1, const __grid_constant__ CUtensorMap tm_s0,
@@ -218,14 +222,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int R = p.R, NS = p.stages;
-    const uint32_t x_bytes = R * 256;
+    const uint32_t x_bytes = WIDE ? R * 128 : R * 256;
+    const int NX = WIDE ? kHalves : NS;
+    constexpr int kABase = WIDE ? 2 * kWideRows : 256;  // TMEM column of the A slots, and of a slot
+    constexpr int kASlot = WIDE ? 64 : 128, kAOp = kASlot / 2;
     uint8_t* xbase = smem + NS * kStageStride;
-    uint8_t* epi = xbase + NS * x_bytes;
+    uint8_t* epi = xbase + NX * x_bytes;
     Aux& aux = *reinterpret_cast<Aux*>(epi + kEpiBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int* abort_flag = &aux.abort_flag;
     const uint64_t wait_ns = p.wait_ns;
-    const int nbuf = R <= 64 ? 2 : 1;
+    const int nbuf = WIDE ? 1 : (R <= 64 ? 2 : 1);
+    const uint32_t d_op = WIDE ? kWideRows : (nbuf == 2 ? 64 : 128);  // from the first operand's accumulator to the second's
 
     if (warp == kCodeProducer && lane == 0) {
         for (int s = 0; s < kMaxStages; ++s) {
@@ -358,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int e, first, rows, cb;
             decode_tile(aux, E, R, tile, e, first, rows, cb);
             const int x_row = aux.off[e] + first;
-            for (int kb = 0; kb < nk; ++kb) {
+            for (int kb = 0; kb < (WIDE ? 2 * nk : nk); ++kb) {
                 if (!quick_wait(smem_u32(&aux.done[xs]), ph ^ 1u, abort_flag, wait_ns)) {
                     give_up();
                     ok = false;
@@ -368,13 +376,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t full = smem_u32(&aux.ready[xs]);
                     const uint32_t x = smem_u32(xbase + xs * x_bytes);
                     mbar_expect_tx(full, x_bytes);
-                    tma_load_2d(x, &tm_x, kb * kCols, x_row, full);
-                    tma_load_2d(x + R * 128, &tm_x, kb * kCols + 64, x_row, full);
+                    if (WIDE) {
+                        tma_load_2d(x, &tm_x, kb * 64, x_row, full);
+                    } else {
+                        tma_load_2d(x, &tm_x, kb * kCols, x_row, full);
+                        tma_load_2d(x + R * 128, &tm_x, kb * kCols + 64, x_row, full);
+                    }
                 }
                 __syncwarp();
                 used |= 1u << xs;
                 last = (last & ~(1u << xs)) | (ph << xs);
-                if (++xs == NS) {
+                if (++xs == NX) {
                     xs = 0;
                     ph ^= 1u;
                 }
@@ -393,12 +405,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             decode_tile(aux, E, R, tile, e, first, rows, cb);
             const uint32_t idesc = idesc_bf16(128, (rows + 15) & ~15);
             const uint32_t buf = nbuf == 2 ? (j & 1u) : 0u, use = nbuf == 2 ? j >> 1 : j;
-            const uint32_t d0 = tmem_base + buf * 128, d1 = d0 + (nbuf == 2 ? 64 : 128);
+            const uint32_t d0 = tmem_base + buf * 128, d1 = d0 + d_op;
             if (!quick_wait(smem_u32(&aux.tempty[buf]), (use & 1u) ^ 1u, abort_flag, wait_ns)) {
                 give_up();
                 break;
             }
-            for (int kb = 0; kb < nk && ok; ++kb) {
+            for (int kb = 0; kb < (WIDE ? 2 * nk : nk) && ok; ++kb) {
                 if (!quick_wait(smem_u32(&aux.ready[xs]), xph, abort_flag, wait_ns)) {
                     give_up();
                     ok = false;
@@ -406,26 +418,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t a = tmem_base + 256 + slot * 128;
+                    constexpr int STEPS = WIDE ? 4 : 8;  // 16-column steps of a slot
+                    const uint32_t a = tmem_base + kABase + slot * kASlot;
                     const uint32_t x = smem_u32(xbase + xs * x_bytes);
                     const uint64_t b0 = sdesc_sw128(x), b1 = sdesc_sw128(x + R * 128);
-                    const int left = p.K - kb * kCols;  // a multiple of 32
-                    if (kb == 0) mma_step<false>(d0, d1, a, b0, idesc);
-                    else mma_step<true>(d0, d1, a, b0, idesc);
-                    mma_step<true>(d0, d1, a + 8, b0 + 2, idesc);
-                    if (left >= kCols) {
+                    const int left = p.K - kb * (16 * STEPS);  // a multiple of 32; a wide tile's last half may have none
+                    if (left > 0) {
+                        if (kb == 0) mma_step<false, kAOp>(d0, d1, a, b0, idesc);
+                        else mma_step<true, kAOp>(d0, d1, a, b0, idesc);
+                        mma_step<true, kAOp>(d0, d1, a + 8, b0 + 2, idesc);
+                        if (left >= 16 * STEPS) {
 #pragma unroll
-                        for (int kk = 2; kk < 8; ++kk)
-                            mma_step<true>(d0, d1, a + kk * 8, (kk < 4 ? b0 : b1) + (kk & 3) * 2, idesc);
-                    } else {
-                        for (int kk = 2; kk < left / 16; ++kk)
-                            mma_step<true>(d0, d1, a + kk * 8, (kk < 4 ? b0 : b1) + (kk & 3) * 2, idesc);
+                            for (int kk = 2; kk < STEPS; ++kk)
+                                mma_step<true, kAOp>(d0, d1, a + kk * 8, (kk < 4 ? b0 : b1) + (kk & 3) * 2, idesc);
+                        } else {
+                            for (int kk = 2; kk < left / 16; ++kk)
+                                mma_step<true, kAOp>(d0, d1, a + kk * 8, (kk < 4 ? b0 : b1) + (kk & 3) * 2, idesc);
+                        }
                     }
                     tc_commit(smem_u32(&aux.done[xs]));
                 }
                 __syncwarp();
                 slot ^= 1u;
-                if (++xs == NS) {
+                if (++xs == NX) {
                     xs = 0;
                     xph ^= 1u;
                 }
@@ -441,7 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < 16) {
         // ================= unpack: a weight row per thread
         const int qw = warp & 3, op = (warp >> 2) & 1, slot = warp >> 3, row = 32 * qw + lane;
-        const uint32_t a_lane = tmem_base + 256 + slot * 128 + op * 64 + ((uint32_t)(32 * qw) << 16);
+        // (a wide tile's slots are halves of a stage)
+        const uint32_t a_lane = tmem_base + kABase + (WIDE ? 0 : slot * kASlot) + op * kAOp + ((uint32_t)(32 * qw) << 16);
         // piece 0 of this row's codes under the 64-byte swizzle; the others differ by an exclusive or
         const uint32_t codes = smem_u32(smem) + op * kOpBytes + row * 64 + (((row >> 1) & 3) << 4);
         const uint8_t* scales = smem + 2 * kOpBytes + op * kScaleBytes + row * 2;
@@ -470,11 +486,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const bool all_fast = __all_sync(0xffffffffu, fast);  // (every lane has read the stage)
             if (lane == 0) mbar_arrive(smem_u32(&aux.cempty[cs]));
-            if (n >= kSlots && !quick_wait(smem_u32(&aux.done[before]), ph_before, abort_flag, wait_ns)) {
-                give_up();
-                break;
+            if (!WIDE) {
+                if (n >= kSlots && !quick_wait(smem_u32(&aux.done[before]), ph_before, abort_flag, wait_ns)) {
+                    give_up();
+                    break;
+                }
+                tc_fence_after();
             }
-            tc_fence_after();
+            // A wide tile's half stage 2 n + h: its token rows are half 2 slot + h of the ring, its A slot is h, and
+            // the half stage two before it (the other set's) frees that slot.
+            const uint32_t turn = (uint32_t)(n / kSlots);
+            bool ok = true;
+            auto store_half = [&](int h, uint32_t (&o)[32]) {
+                if (!WIDE) {
+                    tmem_st32(a_lane + h * 32, o);
+                    return;
+                }
+                if (slot == 1 || turn > 0)
+                    ok = ok && quick_wait(smem_u32(&aux.done[(2 * slot + h + 2) & 3]), (turn - (slot == 0 ? 1u : 0u)) & 1u,
+                                          abort_flag, wait_ns);
+                if (!ok) return;
+                tc_fence_after();
+                tmem_st32(a_lane + h * kASlot, o);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&aux.ready[2 * slot + h]));
+            };
             if (all_fast) {
                 Scale k[NG];
 #pragma unroll
@@ -491,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         unpack_fast(c.z, g, o + 16 * i + 8);
                         unpack_fast(c.w, g, o + 16 * i + 12);
                     }
-                    tmem_st32(a_lane + h * 32, o);
+                    store_half(h, o);
                 }
             } else {
 #pragma unroll
@@ -507,13 +545,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         unpack_slow(c.z, g, o + 16 * i + 8);
                         unpack_slow(c.w, g, o + 16 * i + 12);
                     }
-                    tmem_st32(a_lane + h * 32, o);
+                    store_half(h, o);
                 }
             }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&aux.ready[cs]));
+            if (!ok) {
+                give_up();
+                break;
+            }
+            if (!WIDE) {
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&aux.ready[cs]));
+            }
             before = cs;
             ph_before = ph;
             if ((cs += kSlots) >= NS) {
@@ -537,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t base = aux.off[e] + first;
             const uint32_t buf = nbuf == 2 ? (j & 1u) : 0u, use = nbuf == 2 ? j >> 1 : j;
             const uint32_t lanes = (uint32_t)(32 * qw) << 16;
-            const uint32_t d0 = tmem_base + buf * 128 + lanes, d1 = d0 + (nbuf == 2 ? 64 : 128);
+            const uint32_t d0 = tmem_base + buf * 128 + lanes, d1 = d0 + d_op;
             if (!quick_wait(smem_u32(&aux.tfull[buf]), use & 1u, abort_flag, wait_ns)) {
                 give_up();
                 break;
@@ -612,10 +656,10 @@ static bool encode(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, ui
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool SWIGLU, int GP, bool ZERO>
-static cudaError_t run(const Ctx& c, const void* x, const W4& w0, const W4& w1, Args a) {
+template <bool SWIGLU, int GP, bool ZERO, bool WIDE>
+static cudaError_t run_tile(const Ctx& c, const void* x, const W4& w0, const W4& w1, Args a) {
     set_wait_args(a);
-    auto kern = grouped_gemm_w4_kernel<SWIGLU, GP, ZERO>;
+    auto kern = grouped_gemm_w4_kernel<SWIGLU, GP, ZERO, WIDE>;
     static bool attr_done[64] = {};
     if (c.device < 0 || c.device >= 64) return cudaErrorInvalidDevice;
     if (!attr_done[c.device]) {
@@ -640,15 +684,22 @@ static cudaError_t run(const Ctx& c, const void* x, const W4& w0, const W4& w1, 
         else tz[i] = ts[i];
     }
     if (!ok) return cudaErrorInvalidValue;
-    // as many stages of codes and token rows as fit (4 at 128 token rows)
-    const int left = kSmemLimit - 1024 - kAuxBytes - kEpiBytes, stage = kStageStride + a.R * 256;
+    // as many stages of codes and token rows as fit
+    const int left = kSmemLimit - 1024 - kAuxBytes - kEpiBytes - (WIDE ? kHalves * a.R * 128 : 0);
+    const int stage = kStageStride + (WIDE ? 0 : a.R * 256);
     a.stages = left / stage < kMaxStages ? left / stage : kMaxStages;
-    static_assert((kSmemLimit - 1024 - kAuxBytes - kEpiBytes) / (kStageStride + 128 * 256) >= kSlots, "stages");
-    const size_t smem = 1024 + (size_t)a.stages * stage + kEpiBytes + kAuxBytes;
+    if (a.stages < kSlots) return cudaErrorInvalidValue;
+    const size_t smem = kSmemLimit - left + (size_t)a.stages * stage;
     const int64_t max_tiles = ((int64_t)a.S / a.R + a.E) * ((a.n_out + WROWS - 1) / WROWS);
     const int grid = (int)(max_tiles < c.num_sms ? max_tiles : c.num_sms);
     if (grid <= 0) return cudaSuccess;
     return launch(kern, dim3(grid), dim3(kThreads), smem, c, tx, tq[0], tq[1], ts[0], ts[1], tz[0], tz[1], a);
+}
+
+template <bool SWIGLU, int GP, bool ZERO>
+static cudaError_t run(const Ctx& c, const void* x, const W4& w0, const W4& w1, const Args& a) {
+    return a.R == kWideRows ? run_tile<SWIGLU, GP, ZERO, true>(c, x, w0, w1, a)
+                            : run_tile<SWIGLU, GP, ZERO, false>(c, x, w0, w1, a);
 }
 
 template <bool SWIGLU>
@@ -658,11 +709,15 @@ static cudaError_t run_group(const Ctx& c, const void* x, const W4& w0, const W4
     return w0.z ? run<SWIGLU, 4, true>(c, x, w0, w1, a) : run<SWIGLU, 4, false>(c, x, w0, w1, a);
 }
 
-// token rows per tile: the least of 16, 32, 64 and 128 that holds about twice an expert's average, so that few
-// experts need a second pass over their weights
+// Token rows per tile: few rows take twice an expert's average, so that few experts need a second pass over their
+// weights.  From 128 on tiles of 128 or of 192 rows, whichever needs fewer passes: a wide tile costs more (its rings
+// turn in half stages: 104 against 88 us at 120 rows, gate/up of 32 experts of 1536 x 4096), but at 128..176 rows it is
+// one pass for most experts where narrow ones are two (117 against 139 us at 160), and past 384 its fewer passes are 2-6%
+// (301 against 321 us at 512); between, both take the same number and narrow ones win (163 against 151 us at 208).
 static int tile_rows(int S, int E) {
     const int avg = S / E;
-    return avg <= 8 ? 16 : (avg <= 16 ? 32 : (avg <= 40 ? 64 : 128));
+    if (avg <= 40) return avg <= 8 ? 16 : (avg <= 16 ? 32 : 64);
+    return (avg >= 128 && avg <= 176) || avg > 384 ? kWideRows : 128;
 }
 
 static Args base_args(const int32_t* counts, const int32_t* offsets, int S, int E, int K, int n_out, int group, void* out,

@@ -114,6 +114,8 @@ COUNTS = {
     "empty": [0, 0, 0],
     "many": [130, 0, 64, 257, 3, 16],
     "large": [500, 129, 300],
+    "wide": [192, 120, 193, 130],
+    "widest": [400, 385, 577],
 }
 
 
