@@ -99,7 +99,7 @@ typedef struct {
 } moe_weights_fp8_t;
 
 /* 4-bit weights with group scales (see moe_quantize_w4): the matrix w[n][k] of every expert as codes
- * q [E][n][k / 2], scales s [E][G][n] bf16 and zero points z [E][G][n] (NULL: 8 everywhere), where one scale
+ * q [E][n][k / 2], scales s [E][G][n] bf16 and zero points z [E][G][n] (0..15, not checked; NULL: 8 everywhere), where one scale
  * and zero point serve `group` consecutive columns of a row and G = ceil(k / group):
  *   w[e][n][j] = (code(e, n, j) - z[e][j / group][n]) * s[e][j / group][n]
  * Eight columns of a row are one little-endian 32-bit word: nibble i (0..3) holds column 2 i, nibble 4 + i

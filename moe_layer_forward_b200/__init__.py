@@ -416,8 +416,8 @@ def moe_forward_fp8(x, gamma, W_r, b, Wg, Wu, Wd, out, top_k: int = 8, eps: floa
 
 # --------------------------------------------------------------------------- 4-bit experts
 class W4Weights(NamedTuple):
-    """A 4-bit expert matrix [E][n][k]: codes q uint8 [E][n][k / 2], scales s bf16 and zero points z uint8 (or None: 8
-    everywhere) [E][ceil(k / group)][n]; see ``moe_w4_t`` in include/moe.h for the layout and ``pack_w4``."""
+    """A 4-bit expert matrix [E][n][k]: codes q uint8 [E][n][k / 2], scales s bf16 and zero points z uint8 0..15 (or
+    None: 8 everywhere) [E][ceil(k / group)][n]; see ``moe_w4_t`` in include/moe.h for the layout and ``pack_w4``."""
 
     q: torch.Tensor
     s: torch.Tensor
@@ -469,6 +469,8 @@ def _expect(name: str, t: torch.Tensor, shape, dtype, dev: int):
 def _w4(name: str, w: W4Weights, E: int, n: int, k: int, dev: int):
     """The addresses of a matrix's codes, scales and zero points, once they fit E x n x k."""
     q, s, z, group = w
+    if group not in (32, 64, 128):
+        raise ValueError(f"{name} has groups of {group} columns, expected 32, 64 or 128")
     sizes = (E, -(-k // group), n)
     return (_expect(name, q, (E, n, k // 2), torch.uint8, dev),
             _expect(name, s, sizes, torch.bfloat16, dev),

@@ -25,7 +25,7 @@
 //                of the two operands.  A piece is transposed through 2 KB of shared memory of the warp's own.
 //   warp 24, 25  TMA producers: a ring of code stages (128 columns of both operands, scales, zero points) and one of
 //                token stages (R rows x 128 columns)
-//   warp 26      owns the TMEM allocation; lane 0 issues the MMAs and commits
+//   warp 26      owns the TMEM allocation; one elected lane issues the MMAs and commits
 // Tensor memory: columns 0..255 accumulators (R <= 64: two buffers of gate | up, else one), 256..511 the A slots.  Wide
 // tiles (192 rows): 384 columns of accumulators, and slots of 64 columns of both operands: their token ring and
 // their A slots turn in half stages.

@@ -600,6 +600,7 @@ def test_refusals(moe):
         (ValueError, lambda: moe.moe_expert_gate_up_w4(x, Wg, Wu._replace(group=64), ct, off, h)),
         (moe.MoEError, lambda: moe.moe_expert_gate_up_w4(x, Wg, Wu._replace(z=None), ct, off, h)),
         (ValueError, lambda: moe.moe_expert_gate_up_w4(x, Wg, Wd, ct, off, h)),
+        (ValueError, lambda: moe.moe_expert_down_w4(h, Wd._replace(group=0), ct, off, y)),
         (ValueError, lambda: moe.moe_expert_down_w4(h, Wd._replace(q=Wd.q.cpu()), ct, off, y)),
         (ValueError, lambda: moe.moe_expert_down_w4(h, Wd, ct.cpu(), off, y)),
         (TypeError, lambda: moe.moe_expert_down_w4(h, Wd._replace(s=Wd.s.half()), ct, off, y)),
