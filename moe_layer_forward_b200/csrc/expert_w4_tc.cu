@@ -672,7 +672,7 @@ static cudaError_t run_tile(const Ctx& c, const void* x, const W4& w0, const W4&
     const uint64_t wrows = (uint64_t)a.E * a.n_out, grows = (uint64_t)a.E * a.G;
     bool ok = encode(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, a.K, a.S, (uint64_t)a.K * 2, 64, a.R,
                      CU_TENSOR_MAP_SWIZZLE_128B);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < (SWIGLU ? 2 : 1); ++i) {
         const W4& w = i ? w1 : w0;
         ok = ok && encode(&tq[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, w.q, a.K / 2, wrows, a.K / 2, kCols / 2, 128,
                           CU_TENSOR_MAP_SWIZZLE_64B);
@@ -682,6 +682,11 @@ static cudaError_t run_tile(const Ctx& c, const void* x, const W4& w0, const W4&
             ok = ok && encode(&tz[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, w.z, a.n_out, grows, a.n_out, 128, NG,
                               CU_TENSOR_MAP_SWIZZLE_NONE);
         else tz[i] = ts[i];
+    }
+    if (!SWIGLU) {  // both operands are rows of one matrix
+        tq[1] = tq[0];
+        ts[1] = ts[0];
+        tz[1] = tz[0];
     }
     if (!ok) return cudaErrorInvalidValue;
     // as many stages of codes and token rows as fit
