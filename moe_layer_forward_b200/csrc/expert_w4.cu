@@ -524,12 +524,11 @@ __device__ __forceinline__ void stream(const Args& args, const Phase& p, uint8_t
                     xg += GROUP;
                     mg += mrows;
                 };
-                if ((st + 1) * NG <= p.G) {
+                const int ng = p.G - st * NG;
 #pragma unroll
-                    for (int gi = 0; gi < NG; ++gi) do_group(gi);
-                } else {
-#pragma unroll 1
-                    for (int gi = 0; gi < p.G - st * NG; ++gi) do_group(gi);
+                for (int gi = 0; gi < NG; ++gi) {
+                    if (gi >= ng) break;
+                    do_group(gi);
                 }
                 __syncwarp();  // every lane has read the slot that the next copies overwrite
                 if (++slot == kStages) slot = 0;
