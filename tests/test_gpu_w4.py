@@ -238,6 +238,35 @@ def test_grouped_long_rows_many_of_them(moe):
     assert any(right(*m) for m in ref.readings(Wg, Wu))
 
 
+@pytest.mark.parametrize("counts,S", [([0, 0], 200), ([0] * 256, 256), ([1] * 256, 256), ([300], 300), ([1], 1),
+                                      ([0, 0, 0, 1], 2000), ([40] * 5, 4000)])
+def test_grouped_extremes_of_experts_and_rows(moe, counts, S):
+    """One expert and 256, none of the buffers' rows used, or few of many."""
+    gen = torch.Generator().manual_seed(S)
+    ct, off, used = segments(counts)
+    E, d, f = len(counts), 64, 96
+    W = [weights(gen, E, n, k, 32, True) for n, k in ((f, d), (f, d), (d, f))]
+    x = torch.randn((S, d), generator=gen).to(BF)
+    h, y = torch.full((S, f), 9.0, dtype=BF, device=DEV), torch.full((S, d), 9.0, dtype=BF, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    moe.moe_grouped_swiglu_w4(x.to(DEV), *[put(moe, m) for m in W], ct.to(DEV), off.to(DEV), h, y, dev_status=status)
+    assert status.item() == 0
+    h, y = h.cpu().double(), y.cpu().double()
+    assert (h[used:] == 9).all() and (y[used:] == 9).all()
+
+    def right(wg, wu, wd):
+        ok = True
+        for e, n in enumerate(counts):
+            if n:
+                r = slice(int(off[e]), int(off[e]) + n)
+                hr, dh = ref.gate_up(x[r].double(), wg[e], wu[e], 32)
+                ok &= ref.within(h[r], hr, dh, 2.0 ** -8)
+                ok &= ref.within(y[r], h[r] @ wd[e].T, ref.product_bound(h[r], wd[e], 32), 2.0 ** -8)
+        return ok
+
+    assert any(right(*m) for m in ref.readings(*W))
+
+
 def test_grouped_waits_that_run_out(moe):
     """As for the other tensor-core kernels: a stalled wait gives up, is reported, and the next call is right."""
     gen = torch.Generator().manual_seed(16)
